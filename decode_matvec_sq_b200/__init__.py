@@ -27,6 +27,8 @@ SQ_LAYOUT_ROWS = 0
 SQ_LAYOUT_TILES = 1
 SQ_LAYOUT_TILES_SPARSE = 2
 SQ_LAYOUT_TILES_ASYM = 3
+SQ_GATE_TOPK = 0
+SQ_GATE_ALL = 1
 
 STATUS = {
     0: "SQ_OK", 1: "SQ_ERR_INVALID_ARG", 2: "SQ_ERR_SHAPE", 3: "SQ_ERR_ALIGN",
@@ -106,6 +108,11 @@ def lib():
                                    ctypes.c_int),
         "sq_linear_noalloc": ([pw, vp, vp, vp, vp, i32, i32, vp, vp, u32, vp], ctypes.c_int),
         "sq_quantize_linear": ([pw, vp, i32, vp, i32, vp, vp, sz, vp, u32, vp], ctypes.c_int),
+        "sq_route_workspace_bytes": ([i32, i32, i32], sz),
+        "sq_route": ([vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp, u32, vp], ctypes.c_int),
+        "sq_segment_workspace_bytes": ([i32, i32], sz),
+        "sq_segment": ([vp, i32, i32, vp, vp, vp, vp, sz, vp, u32, vp], ctypes.c_int),
+        "sq_combine": ([vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, u32, vp], ctypes.c_int),
         "sq_testing_prefill_stalled": ([pw, vp, vp, vp, vp, i32, i32, vp, i32, ctypes.c_uint64, vp,
                                         vp], ctypes.c_int),
     }
@@ -542,6 +549,125 @@ def testing_nvfp4_stalled(w: Nvfp4Matrix, x: Nvfp4Matrix, y, skip_stage: int, wa
     requested and every wait limited to wait_ns (tests of the timeout path)."""
     _ck(lib().sq_testing_nvfp4_stalled(ctypes.byref(w.view), ctypes.byref(x.view), _ptr(y), skip_stage,
                                        wait_ns, _ptr(status), _stream(stream)), "sq_testing_nvfp4_stalled")
+
+
+# ---- weights that depend on the token (include/sq.h documents the arrays) -----
+
+def _refuse(where: str, what: str, code: str = "SQ_ERR_INVALID_ARG"):
+    raise SQError(STATUS_CODE[code], f"{where}: {what}")
+
+
+def _arg(t, dtype, shape, where: str, name: str) -> int:
+    """The address of a tensor argument: a contiguous CUDA tensor of this type
+    and shape on the current device, else the call is refused."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _refuse(where, f"{name} must be a contiguous CUDA tensor of {dtype}")
+    if tuple(t.shape) != shape:
+        _refuse(where, f"{name} must be {list(shape)}, got {list(t.shape)}", "SQ_ERR_SHAPE")
+    if t.get_device() != torch.cuda.current_device():
+        _refuse(where, f"{name} is not on the current device")
+    return t.data_ptr()
+
+
+def _opt(t, dtype, shape, where: str, name: str):
+    return None if t is None else _arg(t, dtype, shape, where, name)
+
+
+def _status_arg(status, where: str):
+    import torch
+    return _opt(status, torch.int32, (1,), where, "status")
+
+
+def _workspace_arg(ws, need: int, device, where: str):
+    """(tensor, address, bytes) of a uint8 workspace of at least `need` bytes;
+    allocated here when the caller keeps none."""
+    import torch
+    if ws is None:
+        if not need:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws, _arg(ws, torch.uint8, (ws.numel(),), where, "workspace"), ws.numel()
+
+
+@dataclass
+class Segments:
+    """Entries sorted by id: segment s is the places offsets[s] .. offsets[s+1]."""
+    offsets: object   # [S + 1] int32
+    order: object     # [n] int32: the entry at each place, -1 behind the last segment
+    place: object     # the place of each entry, -1 without an id
+
+
+@dataclass
+class Route(Segments):
+    ids: object       # [T][k] int32
+    gates: object     # [T][k] float32
+
+
+def route(logits, k: int, gate: str = "topk", workspace=None, status=None, pdl: bool = False,
+          stream=None) -> Route:
+    """Top-k of logits [T][E] (float32) with softmax gates over the chosen
+    ("topk") or over all experts ("all"), and the entries sorted by expert."""
+    import torch
+    if gate not in ("topk", "all"):
+        _refuse("sq_route", 'gate must be "topk" or "all"')
+    if logits.dim() != 2:
+        _refuse("sq_route", "logits must be [T][E]", "SQ_ERR_SHAPE")
+    T, E = logits.shape
+    lp = _arg(logits, torch.float32, (T, E), "sq_route", "logits")
+    if not 1 <= k <= 32 or T < 1 or T * k > 1 << 24:
+        _refuse("sq_route", "T or k", "SQ_ERR_SHAPE")
+    dev, i32 = logits.device, torch.int32
+    ids = torch.empty(T, k, dtype=i32, device=dev)
+    gates = torch.empty(T, k, dtype=torch.float32, device=dev)
+    offsets = torch.empty(E + 1, dtype=i32, device=dev)
+    order = torch.empty(T * k, dtype=i32, device=dev)
+    place = torch.empty(T, k, dtype=i32, device=dev)
+    L = lib()
+    ws, wp, wn = _workspace_arg(workspace, int(L.sq_route_workspace_bytes(T, E, k)), dev, "sq_route")
+    _ck(L.sq_route(lp, T, E, k, SQ_GATE_ALL if gate == "all" else SQ_GATE_TOPK, ids.data_ptr(),
+                   gates.data_ptr(), offsets.data_ptr(), order.data_ptr(), place.data_ptr(), wp, wn,
+                   _status_arg(status, "sq_route"), _flags(pdl), _stream(stream)), "sq_route")
+    return Route(offsets, order, place, ids, gates)
+
+
+def segment(ids, S: int, workspace=None, status=None, pdl: bool = False, stream=None) -> Segments:
+    """Entries with ids (int32, any shape, -1 = none) in [0, S) sorted by id."""
+    import torch
+    n = ids.numel()
+    ip = _arg(ids, torch.int32, tuple(ids.shape), "sq_segment", "ids")
+    if not 1 <= S <= 1024 or not 1 <= n <= 1 << 24:
+        _refuse("sq_segment", "n or S", "SQ_ERR_SHAPE")
+    dev = ids.device
+    offsets = torch.empty(S + 1, dtype=torch.int32, device=dev)
+    order = torch.empty(n, dtype=torch.int32, device=dev)
+    place = torch.empty(ids.shape, dtype=torch.int32, device=dev)
+    L = lib()
+    ws, wp, wn = _workspace_arg(workspace, int(L.sq_segment_workspace_bytes(n, S)), dev, "sq_segment")
+    _ck(L.sq_segment(ip, n, S, offsets.data_ptr(), order.data_ptr(), place.data_ptr(), wp, wn,
+                     _status_arg(status, "sq_segment"), _flags(pdl), _stream(stream)), "sq_segment")
+    return Segments(offsets, order, place)
+
+
+def combine(z, gates, place, base=None, out=None, status=None, pdl: bool = False, stream=None):
+    """out [T][N] = base + sum_j gates[t][j] * z[place[t][j]] (float32); place -1
+    adds nothing.  out may be base, not z."""
+    import torch
+    w = "sq_combine"
+    if z.dim() != 2 or gates.dim() != 2:
+        _refuse(w, "z must be [rows][N] and gates [T][k]", "SQ_ERR_SHAPE")
+    rows, N = z.shape
+    T, k = gates.shape
+    zp = _arg(z, torch.float32, (rows, N), w, "z")
+    gp = _arg(gates, torch.float32, (T, k), w, "gates")
+    pp = _arg(place, torch.int32, (T, k), w, "place")
+    bp = _opt(base, torch.float32, (T, N), w, "base")
+    if out is None:
+        out = torch.empty(T, N, dtype=torch.float32, device=z.device)
+    op = _arg(out, torch.float32, (T, N), w, "out")
+    _ck(lib().sq_combine(zp, rows, gp, pp, T, k, N, bp, op, _status_arg(status, w), _flags(pdl),
+                         _stream(stream)), w)
+    return out
 
 
 def testing_read_peak(buf, iters: int = 20, stream=None) -> float:

@@ -38,6 +38,7 @@ SOURCES = [
     ("sq_prefill.cu", []),
     ("sq_nvfp4.cu", ["-fmad=false"]),
     ("sq_probe.cu", []),
+    ("sq_route.cu", []),
 ]
 
 

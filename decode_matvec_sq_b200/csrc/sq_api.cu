@@ -615,6 +615,75 @@ sq_status sq_nvfp4_linear(const sq_nvfp4_matrix* w, const sq_nvfp4_matrix* x, fl
   return from_cuda(launch_nvfp4_gemm(*w, *x, y, dev_status, static_cast<cudaStream_t>(stream)));
 }
 
+// ---- weights that depend on the token --------------------------------------------
+
+static constexpr int64_t kMaxEntries = 1 << 24;
+
+static bool route_shape(int64_t T, int64_t E, int64_t k) {
+  return T >= 1 && E >= 1 && E <= kMaxSegments && k >= 1 && k <= kMaxChoices && k <= E && T * k <= kMaxEntries;
+}
+
+size_t sq_route_workspace_bytes(int32_t T, int32_t E, int32_t k) {
+  return route_shape(T, E, k) ? segment_workspace_bytes((int64_t)T * k, E, k, true) : 0;
+}
+
+sq_status sq_route(const float* logits, int32_t T, int32_t E, int32_t k, int32_t gate, int32_t* ids,
+                   float* gates, int32_t* offsets, int32_t* order, int32_t* place, void* workspace,
+                   size_t ws_bytes, int32_t* dev_status, uint32_t flags, void* stream) {
+  if (!logits || !ids || !gates || !offsets || !order || !place) return SQ_ERR_INVALID_ARG;
+  if (!route_shape(T, E, k)) return SQ_ERR_SHAPE;
+  if ((gate != SQ_GATE_TOPK && gate != SQ_GATE_ALL) || (flags & ~SQ_LAUNCH_PDL)) return SQ_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(ids) || !aligned16(gates) || !aligned16(offsets) || !aligned16(order) ||
+      !aligned16(place) || (workspace && !aligned16(workspace)))
+    return SQ_ERR_ALIGN;
+  const size_t need = sq_route_workspace_bytes(T, E, k);
+  if (need && (!workspace || ws_bytes < need)) return SQ_ERR_WORKSPACE;
+  DeviceInfo d;
+  sq_status st = check_device(&d);
+  if (st != SQ_OK) return st;
+  return from_cuda(launch_route(logits, T, E, k, gate == SQ_GATE_ALL, ids, gates, offsets, order, place, workspace,
+                                dev_status, (flags & SQ_LAUNCH_PDL) != 0, static_cast<cudaStream_t>(stream)));
+}
+
+static bool segment_shape(int64_t n, int64_t S) { return n >= 1 && n <= kMaxEntries && S >= 1 && S <= kMaxSegments; }
+
+size_t sq_segment_workspace_bytes(int32_t n, int32_t S) {
+  return segment_shape(n, S) ? segment_workspace_bytes(n, S, 1, false) : 0;
+}
+
+sq_status sq_segment(const int32_t* ids, int32_t n, int32_t S, int32_t* offsets, int32_t* order, int32_t* place,
+                     void* workspace, size_t ws_bytes, int32_t* dev_status, uint32_t flags, void* stream) {
+  if (!ids || !offsets || !order || !place) return SQ_ERR_INVALID_ARG;
+  if (!segment_shape(n, S)) return SQ_ERR_SHAPE;
+  if (flags & ~SQ_LAUNCH_PDL) return SQ_ERR_INVALID_ARG;
+  if (!aligned16(ids) || !aligned16(offsets) || !aligned16(order) || !aligned16(place) ||
+      (workspace && !aligned16(workspace)))
+    return SQ_ERR_ALIGN;
+  const size_t need = sq_segment_workspace_bytes(n, S);
+  if (need && (!workspace || ws_bytes < need)) return SQ_ERR_WORKSPACE;
+  DeviceInfo d;
+  sq_status st = check_device(&d);
+  if (st != SQ_OK) return st;
+  return from_cuda(launch_segment(ids, n, S, offsets, order, place, workspace, dev_status,
+                                  (flags & SQ_LAUNCH_PDL) != 0, static_cast<cudaStream_t>(stream)));
+}
+
+sq_status sq_combine(const float* z, int32_t rows, const float* gates, const int32_t* place, int32_t T, int32_t k,
+                     int32_t N, const float* base, float* out, int32_t* dev_status, uint32_t flags, void* stream) {
+  if (!z || !gates || !place || !out) return SQ_ERR_INVALID_ARG;
+  if (T < 1 || k < 1 || k > kMaxChoices || (int64_t)T * k > kMaxEntries || N < 1 || N > (1 << 24) || rows < 1 ||
+      rows > kMaxEntries)
+    return SQ_ERR_SHAPE;
+  if (flags & ~SQ_LAUNCH_PDL) return SQ_ERR_INVALID_ARG;
+  if (!aligned16(z) || !aligned16(gates) || !aligned16(place) || !aligned16(out) || (base && !aligned16(base)))
+    return SQ_ERR_ALIGN;
+  DeviceInfo d;
+  sq_status st = check_device(&d);
+  if (st != SQ_OK) return st;
+  return from_cuda(launch_combine(z, rows, gates, place, T, k, N, base, out, dev_status, (flags & SQ_LAUNCH_PDL) != 0,
+                                  static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"
 
 // ---- failure injection for the tests (include/sq_testing.h) -----------------------

@@ -116,4 +116,20 @@ cudaError_t launch_prefill(const sq_packed_weight& w, int M, const int8_t* xq, c
                            int32_t* T_out, int32_t* R_out, int32_t* status, cudaStream_t stream,
                            uint64_t wait_ns = 1000000000ull, int skip_group = -1);
 
+// Weights that depend on the token (sq_route.cu).  Workspace of a sort of n
+// entries into S segments: 0 where one CTA does it.  unit: entries per token of
+// a routed sort (route = true), else 1.
+constexpr int kMaxSegments = 1024;
+constexpr int kMaxChoices = 32;
+size_t segment_workspace_bytes(int64_t n, int S, int unit, bool route);
+cudaError_t launch_route(const float* logits, int T, int E, int k, bool all, int32_t* ids,
+                         float* gates, int32_t* offsets, int32_t* order, int32_t* place,
+                         void* workspace, int32_t* status, bool pdl, cudaStream_t stream);
+cudaError_t launch_segment(const int32_t* ids, int n, int S, int32_t* offsets, int32_t* order,
+                           int32_t* place, void* workspace, int32_t* status, bool pdl,
+                           cudaStream_t stream);
+cudaError_t launch_combine(const float* z, int rows, const float* gates, const int32_t* place,
+                           int T, int k, int N, const float* base, float* out, int32_t* status,
+                           bool pdl, cudaStream_t stream);
+
 }  // namespace sq

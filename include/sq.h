@@ -473,6 +473,72 @@ sq_status sq_nvfp4_quantize(const float *X, const sq_nvfp4_matrix *out, int32_t 
 sq_status sq_nvfp4_linear(const sq_nvfp4_matrix *w, const sq_nvfp4_matrix *x, float *y,
                           int32_t *dev_status, void *stream);
 
+/* ---- weights that depend on the token --------------------------------------
+ * A layer of experts (and a set of adapters) holds many weights, and each token
+ * names the ones it meets.  The calls below have no counterpart on the pages;
+ * the experts' products are those of sq_linear.
+ *
+ * An "entry" is one (token, choice) pair; entry t*k + j is choice j of token t.
+ * A sort of entries by their id (expert or adapter, in [0, S)) is three arrays:
+ *   offsets  [S+1] i32  segment s is the places [offsets[s], offsets[s+1])
+ *   order    [n] i32    the entry at each place; within a segment ascending;
+ *                       -1 at the places offsets[S] .. n-1 (entries without an
+ *                       id have no place)
+ *   place    [n] i32    the place of each entry, -1 for an entry without an id
+ */
+
+/* Softmax over the chosen experts, or over all of a token's experts. */
+#define SQ_GATE_TOPK 0
+#define SQ_GATE_ALL 1
+
+/*
+ * The router: per token the k largest logits (ties: the lower expert), their
+ * softmax gates, and the sort of the T*k entries by expert.
+ *   logits     [T][E] f32, device; 1 <= E <= 1024, 1 <= k <= min(E, 32),
+ *              T*k <= 2^24
+ *   gate       SQ_GATE_TOPK: exp(l_j) / sum over the k chosen of exp(l);
+ *              SQ_GATE_ALL: the same over all E experts
+ *   ids        [T][k] i32 out, largest logit first
+ *   gates      [T][k] f32 out
+ *   offsets, order, place   the sort of the entries (above)
+ *   workspace  sq_route_workspace_bytes(T, E, k) bytes (may be 0: then unused)
+ * An expert with logit -inf is masked: it is never chosen.  A token with fewer
+ * than k unmasked experts has id -1 and gate 0 in its last choices.  NaN counts
+ * as masked and sets SQ_ERR_NONFINITE, as does +inf (chosen first; its gate is
+ * the limit: 1 shared by the +inf experts).
+ * flags: SQ_LAUNCH_PDL.
+ */
+size_t sq_route_workspace_bytes(int32_t T, int32_t E, int32_t k);
+sq_status sq_route(const float *logits, int32_t T, int32_t E, int32_t k, int32_t gate, int32_t *ids,
+                   float *gates, int32_t *offsets, int32_t *order, int32_t *place, void *workspace,
+                   size_t ws_bytes, int32_t *dev_status, uint32_t flags, void *stream);
+
+/*
+ * The sort alone: ids [n] i32, device, in [-1, S), -1 = none (anything else
+ * counts as -1 and sets SQ_ERR_INVALID_ARG).  1 <= n <= 2^24, 1 <= S <= 1024.
+ * Workspace: sq_segment_workspace_bytes(n, S) bytes (may be 0).
+ * flags: SQ_LAUNCH_PDL.
+ */
+size_t sq_segment_workspace_bytes(int32_t n, int32_t S);
+sq_status sq_segment(const int32_t *ids, int32_t n, int32_t S, int32_t *offsets, int32_t *order,
+                     int32_t *place, void *workspace, size_t ws_bytes, int32_t *dev_status,
+                     uint32_t flags, void *stream);
+
+/*
+ * The experts' rows back to their tokens:
+ *   out[t][:] = base[t][:] + sum_j gates[t][j] * z[place[t][j]][:]
+ *   z      [rows][N] f32: the rows of sq_grouped_linear, in place order
+ *   gates  [T][k] f32, place [T][k] i32 (-1: the entry adds nothing, and its gate
+ *          is not used; a place outside [-1, rows) counts as -1 and sets
+ *          SQ_ERR_INVALID_ARG)
+ *   base   [T][N] f32, or NULL (then 0); may be out itself
+ *   out    [T][N] f32; may not overlap z
+ * Binary32 sums over j in ascending order.  1 <= k <= 32.  flags: SQ_LAUNCH_PDL.
+ */
+sq_status sq_combine(const float *z, int32_t rows, const float *gates, const int32_t *place,
+                     int32_t T, int32_t k, int32_t N, const float *base, float *out,
+                     int32_t *dev_status, uint32_t flags, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
