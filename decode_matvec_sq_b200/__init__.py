@@ -112,6 +112,10 @@ def lib():
         "sq_route": ([vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp, u32, vp], ctypes.c_int),
         "sq_segment_workspace_bytes": ([i32, i32], sz),
         "sq_segment": ([vp, i32, i32, vp, vp, vp, vp, sz, vp, u32, vp], ctypes.c_int),
+        "sq_expert_view": ([pw, i32, i32, i32, pw], ctypes.c_int),
+        "sq_grouped_linear_workspace_bytes": ([pw, i32, i32, i32], sz),
+        "sq_grouped_linear": ([pw, i32, i32, vp, vp, vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, sz, vp, u32, vp],
+                              ctypes.c_int),
         "sq_combine": ([vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, u32, vp], ctypes.c_int),
         "sq_testing_prefill_stalled": ([pw, vp, vp, vp, vp, i32, i32, vp, i32, ctypes.c_uint64, vp,
                                         vp], ctypes.c_int),
@@ -647,6 +651,109 @@ def segment(ids, S: int, workspace=None, status=None, pdl: bool = False, stream=
     _ck(L.sq_segment(ip, n, S, offsets.data_ptr(), order.data_ptr(), place.data_ptr(), wp, wn,
                      _status_arg(status, "sq_segment"), _flags(pdl), _stream(stream)), "sq_segment")
     return Segments(offsets, order, place)
+
+
+@dataclass
+class PackedExperts:
+    """E experts of shape [N][K] in one packed weight (include/sq.h
+    sq_expert_view); ``keep`` holds the device tensors its view points into."""
+    E: int
+    N: int
+    K: int
+    view: SqPackedWeight
+    keep: object
+
+    def expert(self, e: int) -> PackedWeight:
+        """Expert e as a packed weight of its own: decompose into it, or use it
+        with every call on one weight."""
+        v = SqPackedWeight()
+        _ck(lib().sq_expert_view(ctypes.byref(self.view), self.E, self.N, e, ctypes.byref(v)),
+            "sq_expert_view")
+        buf = self.keep[0] if len(self.keep) == 1 else None
+        return PackedWeight(self.N, self.K, 128, bool(v.mask_bits), v.layout, buf, v)
+
+
+def alloc_experts(E: int, N: int, K: int, with_mask: bool = False, layout: int = SQ_LAYOUT_TILES,
+                  device=None) -> PackedExperts:
+    """An empty stack of experts: decompose each expert's weight into
+    ``.expert(e)`` (all with, or all without a trunk percentile)."""
+    if layout not in (SQ_LAYOUT_TILES, SQ_LAYOUT_TILES_ASYM):
+        _refuse("alloc_experts", "layout must be tiles or tiles with an asymmetric residual")
+    if E < 1 or E > 1024 or N < 1:
+        _refuse("alloc_experts", "E or N", "SQ_ERR_SHAPE")
+    pw = alloc_packed(E * round_up(N, 16), K, 128, with_mask, layout, device)
+    return PackedExperts(E, N, K, pw.view, (pw.buf,))
+
+
+def experts_from_arrays(E: int, N: int, K: int, sign_bits, alpha, res_q, res_scale, mask_bits=None,
+                        res_zero=None) -> PackedExperts:
+    """A stack over arrays that already lie in device memory in the tiled layout
+    (for instance loaded from a file): int32 sign (and mask) words
+    [E*rows][cols/32], float32 alpha [E*rows], int8 codes [E*rows][cols], float32
+    scales (and int32 zero-points) [E*rows][cols/128], rows = roundup(N, 16),
+    cols = roundup(K, 128).  The arrays are used in place."""
+    import torch
+    w = "experts_from_arrays"
+    if E < 1 or E > 1024 or N < 1 or K < 1:
+        _refuse(w, "E, N or K", "SQ_ERR_SHAPE")
+    rows, cols = E * round_up(N, 16), round_up(K, 128)
+    v = SqPackedWeight()
+    v.N, v.K, v.group_size = rows, K, 128
+    v.layout = SQ_LAYOUT_TILES if res_zero is None else SQ_LAYOUT_TILES_ASYM
+    v.sign_stride, v.res_stride, v.scale_stride = cols // 32, cols, cols // 128
+    v.sign_bits = _arg(sign_bits, torch.int32, (rows, cols // 32), w, "sign_bits")
+    v.mask_bits = _opt(mask_bits, torch.int32, (rows, cols // 32), w, "mask_bits")
+    v.alpha = _arg(alpha, torch.float32, (rows,), w, "alpha")
+    v.res_q = _arg(res_q, torch.int8, (rows, cols), w, "res_q")
+    v.res_scale = _arg(res_scale, torch.float32, (rows, cols // 128), w, "res_scale")
+    v.res_zero = _opt(res_zero, torch.int32, (rows, cols // 128), w, "res_zero")
+    e0 = SqPackedWeight()
+    _ck(lib().sq_expert_view(ctypes.byref(v), E, N, 0, ctypes.byref(e0)), w)  # the library's own checks
+    return PackedExperts(E, N, K, v, (sign_bits, alpha, res_q, res_scale, mask_bits, res_zero))
+
+
+def grouped_workspace_bytes(experts: PackedExperts, n: int) -> int:
+    return int(lib().sq_grouped_linear_workspace_bytes(ctypes.byref(experts.view), experts.E, experts.N, n))
+
+
+def new_grouped_workspace(experts: PackedExperts, n: int, device=None):
+    """A workspace for grouped_linear over up to n places (one per call that may
+    overlap another)."""
+    import torch
+    return torch.empty(max(grouped_workspace_bytes(experts, n), 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def grouped_linear(experts: PackedExperts, xq, sx, x_out, idx, offsets, order=None, div: int = 1, y=None,
+                   workspace=None, status=None, pdl: bool = False, stream=None):
+    """y [n][N] float32: place p of segment e is expert e's weight times the
+    activations (as from quantize_act) of row order[p] // div, or of row p
+    without an order.  Rows from offsets[E] on are not written."""
+    import torch
+    w = "sq_grouped_linear"
+    E, N = experts.E, experts.N
+    if xq.dim() != 2:
+        _refuse(w, "xq must be [rows][roundup(K,128)]", "SQ_ERR_SHAPE")
+    rows, nout = xq.shape[0], 0 if idx is None else idx.numel()
+    xp = _arg(xq, torch.int8, (rows, experts.view.res_stride), w, "xq")
+    sp = _arg(sx, torch.float32, (rows,), w, "sx")
+    op = ip = None
+    if nout:
+        op = _arg(x_out, torch.float32, (rows, nout), w, "x_out")
+        ip = _arg(idx, torch.int32, (nout,), w, "idx")
+    n = rows if order is None else order.numel()
+    dp = _opt(order, torch.int32, (n,), w, "order")
+    fp = _arg(offsets, torch.int32, (E + 1,), w, "offsets")
+    if y is None:
+        y = torch.empty(n, N, dtype=torch.float32, device=xq.device)
+    yp = _arg(y, torch.float32, (n, N), w, "y")
+    L = lib()
+    if workspace is None:
+        workspace, wp, wn = _workspace_arg(None, grouped_workspace_bytes(experts, n), xq.device, w)
+    else:
+        wp, wn = _arg(workspace, torch.uint8, (workspace.numel(),), w, "workspace"), workspace.numel()
+    _ck(L.sq_grouped_linear(ctypes.byref(experts.view), E, N, xp, sp, op, ip, nout, rows, dp, div, fp, n, yp, wp,
+                            wn, _status_arg(status, w), _flags(pdl), _stream(stream)), w)
+    return y
 
 
 def combine(z, gates, place, base=None, out=None, status=None, pdl: bool = False, stream=None):

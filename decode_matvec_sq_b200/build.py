@@ -39,6 +39,7 @@ SOURCES = [
     ("sq_nvfp4.cu", ["-fmad=false"]),
     ("sq_probe.cu", []),
     ("sq_route.cu", []),
+    ("sq_grouped.cu", []),
 ]
 
 

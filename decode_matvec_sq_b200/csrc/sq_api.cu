@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "sq_grouped.cuh"
 #include "sq_internal.h"
 #include "sq_layout.h"
 
@@ -666,6 +667,84 @@ sq_status sq_segment(const int32_t* ids, int32_t n, int32_t S, int32_t* offsets,
   if (st != SQ_OK) return st;
   return from_cuda(launch_segment(ids, n, S, offsets, order, place, workspace, dev_status,
                                   (flags & SQ_LAUNCH_PDL) != 0, static_cast<cudaStream_t>(stream)));
+}
+
+// A stack of E experts of N rows in a layout the grouped kernels read.
+static sq_status check_stack(const sq_packed_weight* w, int32_t E, int32_t N) {
+  sq_status st = check_weight(w);
+  if (st != SQ_OK) return st;
+  if (w->layout != SQ_LAYOUT_TILES && w->layout != SQ_LAYOUT_TILES_ASYM) return SQ_ERR_INVALID_ARG;
+  if (E < 1 || E > kMaxSegments || N < 1 || (int64_t)E * tiles_rows(N) != w->N) return SQ_ERR_SHAPE;
+  return SQ_OK;
+}
+
+sq_status sq_expert_view(const sq_packed_weight* stack, int32_t E, int32_t N, int32_t e, sq_packed_weight* out) {
+  if (!out) return SQ_ERR_INVALID_ARG;
+  sq_status st = check_stack(stack, E, N);
+  if (st != SQ_OK) return st;
+  if (e < 0 || e >= E) return SQ_ERR_INVALID_ARG;
+  const int64_t r = e * tiles_rows(N);
+  *out = *stack;
+  out->N = N;
+  out->sign_bits += r * stack->sign_stride;
+  if (out->mask_bits) out->mask_bits += r * stack->sign_stride;
+  out->alpha += r;
+  out->res_q += r * stack->res_stride;
+  out->res_scale += r * stack->scale_stride;
+  if (out->res_zero) out->res_zero += r * stack->scale_stride;
+  return SQ_OK;
+}
+
+size_t sq_grouped_linear_workspace_bytes(const sq_packed_weight* stack, int32_t E, int32_t N, int32_t n) {
+  if (check_stack(stack, E, N) != SQ_OK || n < 1 || n > kMaxEntries) return 0;
+  return grouped_workspace_bytes(E, N, stack->K, n);
+}
+
+sq_status sq_grouped_linear(const sq_packed_weight* stack, int32_t E, int32_t N, const int8_t* xq, const float* sx,
+                            const float* x_out, const int32_t* idx, int32_t n_out, int32_t rows, const int32_t* order,
+                            int32_t div, const int32_t* offsets, int32_t n, float* y, void* workspace, size_t ws_bytes,
+                            int32_t* dev_status, uint32_t flags, void* stream) {
+  sq_status st = check_stack(stack, E, N);
+  if (st != SQ_OK) return st;
+  if (!xq || !sx || !offsets || !y) return SQ_ERR_INVALID_ARG;
+  if (rows < 1 || rows > kMaxEntries || n < 1 || n > kMaxEntries || div < 1) return SQ_ERR_SHAPE;
+  if (n_out < 0 || n_out > kMaxOutliers || n_out > stack->K) return SQ_ERR_SHAPE;
+  if (n_out > 0 && (!idx || !x_out)) return SQ_ERR_INVALID_ARG;
+  if (flags & ~SQ_LAUNCH_PDL) return SQ_ERR_INVALID_ARG;
+  if (!aligned16(xq) || !aligned16(sx) || !aligned16(offsets) || !aligned16(y) || (order && !aligned16(order)) ||
+      (n_out > 0 && (!aligned16(idx) || !aligned16(x_out))) || (workspace && !aligned16(workspace)))
+    return SQ_ERR_ALIGN;
+  const size_t need = grouped_workspace_bytes(E, N, stack->K, n);
+  if (need && (!workspace || ws_bytes < need)) return SQ_ERR_WORKSPACE;
+  DeviceInfo d;
+  if ((st = check_device(&d)) != SQ_OK) return st;
+  GroupedArgs a;
+  a.res = stack->res_q;
+  a.sign = stack->sign_bits;
+  a.mask = stack->mask_bits;
+  a.alpha = stack->alpha;
+  a.scale = stack->res_scale;
+  a.zero = stack->layout == SQ_LAYOUT_TILES_ASYM ? stack->res_zero : nullptr;
+  a.E = E;
+  a.N = N;
+  a.K = stack->K;
+  a.tpr = (int)(tiles_cols(stack->K) / kTileK);
+  a.rbe = (int)(tiles_rows(N) / kTileRows);
+  a.xq = xq;
+  a.xs = (int)xq_stride_of(stack->K);
+  a.sx = sx;
+  a.xout = x_out;
+  a.idx = idx;
+  a.n_out = n_out;
+  a.rows = rows;
+  a.order = order;
+  a.div = div;
+  a.offsets = offsets;
+  a.n = n;
+  a.y = y;
+  a.status = dev_status;
+  a.pdl = (flags & SQ_LAUNCH_PDL) ? 1 : 0;
+  return from_cuda(launch_grouped(a, workspace, d.sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 sq_status sq_combine(const float* z, int32_t rows, const float* gates, const int32_t* place, int32_t T, int32_t k,

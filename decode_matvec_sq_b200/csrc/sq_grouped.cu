@@ -1,0 +1,439 @@
+// sq_grouped.cu -- the linear layer grouped by expert, for the few tokens per
+// expert of a decode step (sm_100a).
+//
+//   y[p] = What_e x[row(p)]   for the places p of segment e,
+// with the products of sq_linear: exact int8 tensor-core sums (mma.sync
+// m16n8k32) of the residual codes per 128-channel group and of the trunk over
+// the row, combined in binary32, outlier channels in binary32.
+//
+// The experts' tiles lie behind one another in the stack, so an expert is a range
+// of row blocks.  A segment is cut into groups of up to 8 NT tokens, which share
+// one read of the expert's weights; the (group, row block) pairs, group-major,
+// are split evenly over the CTAs and a CTA's tiles over its 16 warps, exactly as
+// the decode kernel of one weight splits its own.  Nothing is read for an expert
+// without tokens, and the host needs no counts: every CTA forms the groups from
+// the device's offsets.
+// What bounds it: the weight stream.  Each warp keeps D tiles (2.3 KB each) in
+// flight by bulk copies into its shared-memory ring, one mbarrier per slot.
+// The trunk operand is +-1 (0 outside the mask) bytes made from the bits by one
+// shift, one sign-replicating byte permute and one three-input logic operation
+// per four channels, so T needs one MMA where bits as 0/-1 need two.
+// A lane's 64 code bytes are read as four 16-byte words; lanes 2 and 3 of a quad
+// take them in the order 2, 3, 0, 1 (with their activation words and sign bits
+// swapped alike), which halves the bank conflicts of the unpadded tile.
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "sq_grouped.cuh"
+
+namespace sq {
+namespace {
+
+constexpr int kWarps = 16;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxDepth = 4;
+
+struct Params {
+  GroupedArgs a;
+  int depth;
+  int off_ring, off_part, off_pre, off_ostart;  // shared-memory offsets (bytes)
+};
+
+template <bool MASK, bool ASYM>
+struct Slot {
+  static constexpr int kSign = 2048;
+  static constexpr int kMask = kSign + 256;
+  static constexpr int kScale = MASK ? kMask + 256 : kMask;
+  static constexpr int kZero = kScale + 64;
+  static constexpr int kBytes = ASYM ? kZero + 64 : kZero;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+      "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Byte k = 0xFF if bit 8k+7 of x is set, else 0.
+__device__ __forceinline__ uint32_t sign_bytes(uint32_t x) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, 0, 0xBA98;" : "=r"(d) : "r"(x));
+  return d;
+}
+// Channels 4w .. 4w+3 of a lane's 32 as +1 / -1 bytes, 0 outside the mask.
+template <bool MASK>
+__device__ __forceinline__ uint32_t trunk_word(uint32_t sign, uint32_t mask, int w) {
+  const uint32_t t = ~sign_bytes(sign << (7 - w)) | 0x01010101u;
+  return MASK ? t & sign_bytes(mask << (7 - w)) : t;
+}
+// The bits of words w and w ^ 4 exchanged (bit 8c + w is channel 4w + c).
+__device__ __forceinline__ uint32_t swap_halves(uint32_t b) {
+  return ((b >> 4) & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
+}
+
+// The tokens of one group as a lane sees them.
+template <int NT>
+struct Tokens {
+  const int8_t* x[NT];   // this lane's B column (token gid of each eight), at its 32 channels
+  float sx[NT][2];       // accumulator columns 2 tid4, 2 tid4 + 1
+  int xo[NT][2];         // their rows of x_out
+  int p0, cnt;           // first place, tokens
+};
+
+template <int NT>
+__device__ __forceinline__ void load_tokens(Tokens<NT>& tk, const GroupedArgs& a, int p0, int cnt, int gid, int tid4) {
+  tk.p0 = p0;
+  tk.cnt = cnt;
+#pragma unroll
+  for (int g = 0; g < NT; ++g) {
+    // columns past the group repeat its last token; they are not written
+    tk.x[g] = a.xq + (int64_t)source_row(a, p0 + min(gid + 8 * g, cnt - 1)) * a.xs + tid4 * 32;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = source_row(a, p0 + min(2 * tid4 + c + 8 * g, cnt - 1));
+      tk.sx[g][c] = __ldg(a.sx + r);
+      tk.xo[g][c] = r;
+    }
+  }
+}
+
+template <bool MASK, bool ASYM, int NT>
+__global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
+  using SL = Slot<MASK, ASYM>;
+  constexpr int TG = 8 * NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[kWarps * kMaxDepth];
+  __shared__ int part_i[kWarps];
+  __shared__ int bad_idx;
+  const GroupedArgs& a = p.a;
+  float* part = reinterpret_cast<float*>(smem + p.off_part);  // [kWarps][2][16][TG]
+  int* pre = reinterpret_cast<int*>(smem + p.off_pre);
+  int* ostart = reinterpret_cast<int*>(smem + p.off_ostart);  // first outlier of each channel group
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tid4 = lane & 3;
+  const int D = p.depth;
+
+  if (lane == 0)
+    for (int d = 0; d < D; ++d) mbar_init(&bars[warp * kMaxDepth + d], 1);
+  fence_barrier_init();
+  if (threadIdx.x == 0) bad_idx = 0;
+  __syncthreads();
+  // the outlier list (fixed once a layer is set up), before the wait
+  for (int i = threadIdx.x; i < a.n_out; i += kThreads) {
+    const int j = __ldg(a.idx + i), jp = i > 0 ? __ldg(a.idx + i - 1) : -1;
+    if (j < 0 || j >= a.K || jp >= j) bad_idx = 1;
+  }
+  __syncthreads();
+  const int n_out = bad_idx ? 0 : a.n_out;
+  if (bad_idx && threadIdx.x == 0) set_status(a.status, SQ_ERR_INVALID_ARG);
+  for (int i = threadIdx.x; i < n_out; i += kThreads) {
+    const int g0 = i > 0 ? (__ldg(a.idx + i - 1) >> 7) + 1 : 0, g1 = __ldg(a.idx + i) >> 7;
+    for (int g = g0; g <= g1; ++g) ostart[g] = i;
+  }
+  for (int g = (n_out > 0 ? (__ldg(a.idx + n_out - 1) >> 7) + 1 : 0) + threadIdx.x; g <= a.tpr; g += kThreads)
+    ostart[g] = n_out;
+  if (a.pdl) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+  const int groups = segment_units<kThreads>(a, TG, pre, part_i);
+
+  // the CTA's (group, row block) pairs: the fewest CTAs with the largest share
+  // that one CTA per SM gives
+  const int64_t V = (int64_t)groups * a.rbe;
+  if (V == 0) return;
+  const int64_t share = (V + gridDim.x - 1) / gridDim.x, used = (V + share - 1) / share;
+  if ((int64_t)blockIdx.x >= used) return;
+  const int64_t v0 = blockIdx.x * V / used, v1 = (blockIdx.x + 1) * V / used;
+  const int64_t T0 = v0 * a.tpr, T1 = v1 * a.tpr, len = T1 - T0;
+  const int64_t t0 = T0 + warp * len / kWarps, t1 = T0 + (warp + 1) * len / kWarps;
+
+  // producer cursor: the next tile to copy
+  uint8_t* ring = smem + p.off_ring + warp * D * SL::kBytes;
+  const uint32_t ring_u = smem_u32(ring), bar_u = smem_u32(&bars[warp * kMaxDepth]);
+  int64_t ct = t0, ctile = 0;  // virtual tile, tile in the stack
+  int cleft = 0;               // tiles left in the cursor's group
+  auto seek = [&](int64_t t) {
+    const int64_t vrb = t / a.tpr;
+    const int u = (int)(vrb / a.rbe), e = unit_expert(pre, a.E, u);
+    ctile = ((int64_t)e * a.rbe + vrb % a.rbe) * a.tpr + t % a.tpr;
+    cleft = (int)((int64_t)(u + 1) * a.rbe * a.tpr - t);
+  };
+  auto copy = [&](int slot) {
+    if (ct >= t1) return;
+    if (cleft == 0) seek(ct);
+    const uint32_t dst = ring_u + slot * SL::kBytes, bar = bar_u + 8 * slot;
+    if (lane == 0) mbar_arrive_expect_tx(&bars[warp * kMaxDepth + slot], SL::kBytes);
+    __syncwarp();
+    if (lane == 0) bulk_load(dst, a.res + ctile * 2048, 2048, bar);
+    if (lane == 1) bulk_load(dst + SL::kSign, a.sign + ctile * 64, 256, bar);
+    if (lane == 2) bulk_load(dst + SL::kScale, a.scale + ctile * 16, 64, bar);
+    if (MASK && lane == 3) bulk_load(dst + SL::kMask, a.mask + ctile * 64, 256, bar);
+    if (ASYM && lane == 4) bulk_load(dst + SL::kZero, a.zero + ctile * 16, 64, bar);
+    ++ct;
+    ++ctile;
+    --cleft;
+  };
+  for (int d = 0; d < D; ++d) copy(d);
+
+  const bool hi = tid4 >= 2;  // takes its code words in the order 2, 3, 0, 1
+  const int cofs = lane * 64 + (hi ? 32 : 0), xofs = hi ? 16 : 0;
+  Tokens<NT> tk;
+  int T[NT][4];
+  float F[NT][4], U[NT][4];
+  auto clear = [&] {
+#pragma unroll
+    for (int g = 0; g < NT; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        T[g][i] = 0;
+        F[g][i] = U[g][i] = 0.0f;
+      }
+  };
+  clear();
+  int64_t vrb = t0 / a.tpr;
+  int cg = (int)(t0 - vrb * a.tpr), rb = 0;  // channel group; row block in the expert
+  int64_t erow = 0;                                         // first row of the expert in the stack
+  float al[2] = {0.0f, 0.0f};
+  bool head = cg == 0, timed_out = false;
+  int slot = 0;
+  uint32_t phase = 0;
+
+  // group and row block of virtual row block v
+  auto enter = [&](int64_t v, bool new_group) {
+    if (new_group) {
+      const int u = (int)(v / a.rbe), e = unit_expert(pre, a.E, u);
+      const int2 b = segment_bounds(a, e);
+      const int p0 = b.x + (u - pre[e]) * TG;
+      load_tokens<NT>(tk, a, p0, min(TG, b.y - p0), gid, tid4);
+      rb = (int)(v - (int64_t)u * a.rbe);
+      erow = (int64_t)e * a.rbe * kTileRows;
+    }
+    al[0] = __ldg(a.alpha + erow + rb * kTileRows + gid);
+    al[1] = __ldg(a.alpha + erow + rb * kTileRows + gid + 8);
+  };
+  if (t0 < t1) enter(vrb, true);
+
+  for (int64_t t = t0; t < t1; ++t) {
+    // activation words of this tile (the copies may still be on their way)
+    uint32_t xw[NT][8];
+#pragma unroll
+    for (int g = 0; g < NT; ++g) {
+      const int8_t* xp = tk.x[g] + cg * kTileK;
+      const int4 u = ldg_nc_v4(xp + xofs), v = ldg_nc_v4(xp + (16 - xofs));
+      xw[g][0] = u.x; xw[g][1] = u.y; xw[g][2] = u.z; xw[g][3] = u.w;
+      xw[g][4] = v.x; xw[g][5] = v.y; xw[g][6] = v.z; xw[g][7] = v.w;
+    }
+    const bool landed = mbar_wait(&bars[warp * kMaxDepth + slot], (phase >> slot) & 1u);
+    if (!__all_sync(0xffffffffu, landed)) {
+      timed_out = true;
+      break;
+    }
+    phase ^= 1u << slot;
+    const uint8_t* sl = ring + slot * SL::kBytes;
+    uint32_t q[4][4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const uint4 v = *reinterpret_cast<const uint4*>(sl + ((cofs ^ ((m & 2) << 4)) + (m & 1) * 16));
+      q[m][0] = v.x; q[m][1] = v.y; q[m][2] = v.z; q[m][3] = v.w;
+    }
+    uint2 s = *reinterpret_cast<const uint2*>(sl + SL::kSign + lane * 8);
+    uint2 k = make_uint2(0u, 0u);
+    if constexpr (MASK) k = *reinterpret_cast<const uint2*>(sl + SL::kMask + lane * 8);
+    const float c0 = *reinterpret_cast<const float*>(sl + SL::kScale + gid * 4);
+    const float c1 = *reinterpret_cast<const float*>(sl + SL::kScale + gid * 4 + 32);
+    if (hi) {
+      s.x = swap_halves(s.x);
+      s.y = swap_halves(s.y);
+      if constexpr (MASK) {
+        k.x = swap_halves(k.x);
+        k.y = swap_halves(k.y);
+      }
+    }
+    // R starts at the bits of 1.5 * 2^23, so that R (|R| < 2^22) is read as a float
+    constexpr int kMagic = ASYM ? 0 : 0x4B400000;
+    int R[NT][4], S[NT][4];
+#pragma unroll
+    for (int g = 0; g < NT; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        R[g][i] = kMagic;
+        S[g][i] = 0;
+      }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const uint32_t t0w = trunk_word<MASK>(s.x, k.x, 2 * m), t1w = trunk_word<MASK>(s.y, k.y, 2 * m);
+      const uint32_t t2w = trunk_word<MASK>(s.x, k.x, 2 * m + 1), t3w = trunk_word<MASK>(s.y, k.y, 2 * m + 1);
+#pragma unroll
+      for (int g = 0; g < NT; ++g) {
+        mma_s8(R[g], q[m][0], q[m][1], q[m][2], q[m][3], xw[g][2 * m], xw[g][2 * m + 1]);
+        mma_s8(T[g], t0w, t1w, t2w, t3w, xw[g][2 * m], xw[g][2 * m + 1]);
+        if constexpr (ASYM) {
+          constexpr uint32_t one = 0x01010101u;
+          mma_s8(S[g], one, one, one, one, xw[g][2 * m], xw[g][2 * m + 1]);
+        }
+      }
+    }
+    int z0 = 0, z1 = 0;
+    if constexpr (ASYM) {
+      z0 = *reinterpret_cast<const int*>(sl + SL::kZero + gid * 4);
+      z1 = *reinterpret_cast<const int*>(sl + SL::kZero + gid * 4 + 32);
+    }
+#pragma unroll
+    for (int g = 0; g < NT; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (ASYM) {
+          // the zero-point's part is taken off in whole numbers (z may be large)
+          const long long d = (long long)R[g][i] - (long long)(i < 2 ? z0 : z1) * (long long)S[g][i];
+          F[g][i] = fmaf(i < 2 ? c0 : c1, (float)d, F[g][i]);
+        } else {
+          F[g][i] = fmaf(i < 2 ? c0 : c1, __int_as_float(R[g][i]) - 12582912.0f, F[g][i]);
+        }
+      }
+    // outlier channels of this tile: the dequantized weight of the lane's two
+    // rows from the slot, times its tokens' binary32 activations
+    for (int o = ostart[cg]; o < ostart[cg + 1]; ++o) {
+      const int j = __ldg(a.idx + o) & 127, w = (j & 31) >> 2;
+      const int own = gid * 4 + (j >> 5);
+      const int8_t* cb = reinterpret_cast<const int8_t*>(sl) + own * 64 + (w >> 1) * 16 + (w & 1) * 8 + (j & 3);
+      const uint2 sb = *reinterpret_cast<const uint2*>(sl + SL::kSign + own * 8);
+      const int bit = tiled_bit_of(j & 31);
+      float w0 = ((sb.x >> bit) & 1u) ? al[0] : -al[0], w1 = ((sb.y >> bit) & 1u) ? al[1] : -al[1];
+      if constexpr (MASK) {
+        const uint2 mb = *reinterpret_cast<const uint2*>(sl + SL::kMask + own * 8);
+        w0 = ((mb.x >> bit) & 1u) ? w0 : 0.0f;
+        w1 = ((mb.y >> bit) & 1u) ? w1 : 0.0f;
+      }
+      w0 = fmaf(c0, (float)(cb[0] - z0), w0);
+      w1 = fmaf(c1, (float)(cb[4] - z1), w1);
+#pragma unroll
+      for (int g = 0; g < NT; ++g) {
+        const float x0 = __ldg(a.xout + (int64_t)tk.xo[g][0] * a.n_out + o);
+        const float x1 = __ldg(a.xout + (int64_t)tk.xo[g][1] * a.n_out + o);
+        U[g][0] = fmaf(w0, x0, U[g][0]);
+        U[g][1] = fmaf(w0, x1, U[g][1]);
+        U[g][2] = fmaf(w1, x0, U[g][2]);
+        U[g][3] = fmaf(w1, x1, U[g][3]);
+      }
+    }
+    __syncwarp();  // every lane has read the slot
+    copy(slot);
+    if (++slot == D) slot = 0;
+
+    const bool row_end = cg == a.tpr - 1;
+    if (row_end || t + 1 == t1) {
+      const bool whole = head && row_end;
+#pragma unroll
+      for (int g = 0; g < NT; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = 2 * tid4 + (i & 1) + 8 * g, r = gid + (i >> 1) * 8;
+          const float v = fmaf(tk.sx[g][i & 1], fmaf(al[i >> 1], (float)T[g][i], F[g][i]), U[g][i]);
+          if (c < tk.cnt) {
+            if (whole) {
+              if (rb * kTileRows + r < a.N) a.y[(int64_t)(tk.p0 + c) * a.N + rb * kTileRows + r] = v;
+            } else {
+              // slot 1: the piece that starts its row block; slot 0: one that continues it
+              part[((warp * 2 + (head ? 1 : 0)) * 16 + r) * TG + c] = v;
+            }
+          }
+        }
+      clear();
+      head = true;
+      if (row_end && t + 1 < t1) {
+        ++vrb;
+        ++rb;
+        enter(vrb, rb == a.rbe);
+      }
+    }
+    if (++cg == a.tpr) cg = 0;
+  }
+  if (timed_out) {
+    // the copies in flight end by themselves; wait (bounded) before the CTA leaves
+    if (lane == 0) set_status(a.status, SQ_ERR_TIMEOUT);
+    for (int d = 0; d < D; ++d) (void)mbar_wait(&bars[warp * kMaxDepth + d], (phase >> d) & 1u);
+  }
+  __syncthreads();
+  if (t0 >= t1 || timed_out) return;
+  // the row block that begins in this warp's range and ends past it: the later
+  // warps' parts added in warp order
+  const int64_t last = (t1 - 1) / a.tpr;
+  if (last * a.tpr >= t0 && t1 % a.tpr != 0) {
+    const int64_t end = (last + 1) * a.tpr;
+    int w_hi = warp;
+    while (w_hi + 1 < kWarps && T0 + (w_hi + 1) * len / kWarps < end) ++w_hi;
+#pragma unroll
+    for (int g = 0; g < NT; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = 2 * tid4 + (i & 1) + 8 * g, r = gid + (i >> 1) * 8;
+        if (c >= tk.cnt) continue;
+        float v = part[((warp * 2 + 1) * 16 + r) * TG + c];
+        for (int w = warp + 1; w <= w_hi; ++w)
+          if (T0 + w * len / kWarps < T0 + (w + 1) * len / kWarps) v += part[((w * 2) * 16 + r) * TG + c];
+        if (rb * kTileRows + r < a.N) a.y[(int64_t)(tk.p0 + c) * a.N + rb * kTileRows + r] = v;
+      }
+  }
+}
+
+template <bool MASK, bool ASYM, int NT>
+cudaError_t launch_nt(const GroupedArgs& a, int sm_count, cudaStream_t stream) {
+  using SL = Slot<MASK, ASYM>;
+  constexpr int TG = 8 * NT;
+  Params p;
+  p.a = a;
+  const int part = kWarps * 2 * 16 * TG * 4;
+  const int tables = (int)round_up(4 * (a.E + 1), 16) + (int)round_up(4 * (a.tpr + 1), 16);
+  constexpr int kMax = 227 * 1024 - 2048;
+  p.depth = std::min(kMaxDepth, (kMax - part - tables) / (kWarps * SL::kBytes));
+  if (p.depth < 2) return cudaErrorInvalidValue;
+  p.off_ring = 0;
+  p.off_part = kWarps * p.depth * SL::kBytes;
+  p.off_pre = p.off_part + part;
+  p.off_ostart = p.off_pre + (int)round_up(4 * (a.E + 1), 16);
+  const int smem = p.off_part + part + tables;
+  auto* fn = k_grouped<MASK, ASYM, NT>;
+  const cudaError_t e = ensure_smem_attr((const void*)fn, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t groups = std::min<int64_t>(a.n, a.E + a.n / TG);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(sm_count, groups * a.rbe));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+template <int NT>
+cudaError_t launch_kind(const GroupedArgs& a, int sm_count, cudaStream_t stream) {
+  if (a.zero)
+    return a.mask ? launch_nt<true, true, NT>(a, sm_count, stream) : launch_nt<false, true, NT>(a, sm_count, stream);
+  return a.mask ? launch_nt<true, false, NT>(a, sm_count, stream) : launch_nt<false, false, NT>(a, sm_count, stream);
+}
+
+}  // namespace
+
+size_t grouped_workspace_bytes(int, int, int, int64_t) { return 0; }
+
+cudaError_t launch_grouped(const GroupedArgs& a, void*, int sm_count, cudaStream_t stream) {
+  if (a.n <= 8) return launch_kind<1>(a, sm_count, stream);
+  return launch_kind<2>(a, sm_count, stream);
+}
+
+}  // namespace sq

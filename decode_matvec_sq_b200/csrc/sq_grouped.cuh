@@ -1,0 +1,109 @@
+// sq_grouped.cuh -- arguments and segment bookkeeping shared by the two kernels
+// of the expert-grouped linear layer.
+#pragma once
+
+#include <stdint.h>
+
+#include "sq_common.cuh"
+#include "sq_internal.h"
+#include "sq_layout.h"
+
+namespace sq {
+
+// E experts of N rows (rbe = ceil(N/16) row blocks each) stacked in one tiled
+// weight; n places, the activations' row of place p is order[p] / div (or p).
+struct GroupedArgs {
+  const int8_t* res;
+  const uint32_t* sign;
+  const uint32_t* mask;
+  const float* alpha;
+  const float* scale;
+  const int32_t* zero;
+  int E, N, K, tpr, rbe;
+  const int8_t* xq;
+  int xs;  // row stride of xq
+  const float* sx;
+  const float* xout;
+  const int32_t* idx;
+  int n_out;
+  int rows;             // activation rows
+  const int32_t* order; // may be null
+  int div;
+  const int32_t* offsets;
+  int n;
+  float* y;
+  int32_t* status;
+  int pdl;
+};
+
+// Bounds of segment e, clamped to the n places (offsets that do not ascend in
+// [0, n] are reported; no access leaves the arrays).
+__device__ __forceinline__ int2 segment_bounds(const GroupedArgs& p, int e) {
+  const int a = __ldg(p.offsets + e), b = __ldg(p.offsets + e + 1);
+  const int ca = min(max(a, 0), p.n), cb = min(max(b, ca), p.n);
+  if (ca != a || cb != b) set_status(p.status, SQ_ERR_INVALID_ARG);
+  return make_int2(ca, cb);
+}
+
+// Activation row of place `at`; a row outside the activations is reported and
+// taken as 0.
+__device__ __forceinline__ int source_row(const GroupedArgs& p, int at) {
+  int r = at;
+  if (p.order) {
+    r = __ldg(p.order + at);
+    r = r < 0 ? -1 : r / p.div;
+  }
+  if (r < 0 || r >= p.rows) {
+    set_status(p.status, SQ_ERR_INVALID_ARG);
+    r = 0;
+  }
+  return r;
+}
+
+// Exclusive sums over the experts of ceil(segment / unit), into pre[0 .. E]
+// (shared memory; all threads of the CTA call it; part: one int per warp).
+template <int THREADS>
+__device__ int segment_units(const GroupedArgs& p, int unit, int* pre, int* part) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int carry = 0;
+  for (int e0 = 0; e0 < p.E; e0 += THREADS) {
+    const int e = e0 + (int)threadIdx.x;
+    int v = 0;
+    if (e < p.E) {
+      const int2 b = segment_bounds(p, e);
+      v = (b.y - b.x + unit - 1) / unit;
+    }
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 31) part[warp] = incl;
+    __syncthreads();
+    int before = carry, total = carry;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) before += part[w];
+      total += part[w];
+    }
+    if (e < p.E) pre[e] = before + incl - v;
+    carry = total;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) pre[p.E] = carry;
+  __syncthreads();
+  return carry;
+}
+
+// The expert whose units hold unit u: the last e with pre[e] <= u.
+__device__ __forceinline__ int unit_expert(const int* pre, int E, int u) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+}  // namespace sq

@@ -132,4 +132,9 @@ cudaError_t launch_combine(const float* z, int rows, const float* gates, const i
                            int T, int k, int N, const float* base, float* out, int32_t* status,
                            bool pdl, cudaStream_t stream);
 
+// The expert-grouped linear layer (sq_grouped.cuh holds the arguments).
+struct GroupedArgs;
+size_t grouped_workspace_bytes(int E, int N, int K, int64_t n);
+cudaError_t launch_grouped(const GroupedArgs& a, void* workspace, int sm_count, cudaStream_t stream);
+
 }  // namespace sq

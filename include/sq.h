@@ -525,6 +525,48 @@ sq_status sq_segment(const int32_t *ids, int32_t n, int32_t S, int32_t *offsets,
                      uint32_t flags, void *stream);
 
 /*
+ * A stack of E experts of one shape [N][K]: one packed weight of
+ * E*roundup(N,16) rows in SQ_LAYOUT_TILES or SQ_LAYOUT_TILES_ASYM (sizes and
+ * strides from sq_packed_bytes / sq_packed_view), expert e in its rows
+ * [e*roundup(N,16), ...).  sq_expert_view fills *out with the packed weight of
+ * expert e alone, to decompose into and to use with every call above.
+ * Host-only.  SQ_ERR_SHAPE if the stack's rows are not E*roundup(N,16).
+ */
+sq_status sq_expert_view(const sq_packed_weight *stack, int32_t E, int32_t N, int32_t e,
+                         sq_packed_weight *out);
+
+/*
+ * The linear layer grouped by expert: sq_linear's formula with the weight of
+ * the segment that a place lies in,
+ *   y[p][:] = What_e x[row(p)]   for offsets[e] <= p < offsets[e+1].
+ *   stack, E, N   the experts (above), 1 <= E <= 1024
+ *   xq, sx, x_out, idx, n_out   as written by sq_quantize_act for `rows`
+ *               activation rows; one outlier list for all experts
+ *   order, div  the activation row of place p is order[p] / div (the sort of
+ *               sq_route with div = k), or p itself if order is NULL
+ *   offsets     [E+1] i32, device, ascending from 0; the segments may be empty
+ *   n           places: offsets[E] <= n, order has n entries, 1 <= n <= 2^24
+ *   y           [n][N] f32 out; the rows from offsets[E] on are left as they were
+ *   workspace   sq_grouped_linear_workspace_bytes bytes (may be 0), 16-byte
+ *               aligned; scratch, it needs no zeroing.  Calls that may overlap
+ *               in time (other streams, other captured graphs) need their own.
+ * The weights of experts without places are not read.  The counts stay on the
+ * device: the call neither waits nor copies, and can be captured and replayed on
+ * other routes.  A row's result does not depend on the segments around it, up
+ * to the rounding of binary32 sums.
+ * Device-side findings: offsets that do not ascend in [0, n], an order entry
+ * outside the activation rows and an index list that is not strictly ascending in
+ * [0, K) set SQ_ERR_INVALID_ARG; nothing outside the arrays is touched.
+ * flags: SQ_LAUNCH_PDL.
+ */
+size_t sq_grouped_linear_workspace_bytes(const sq_packed_weight *stack, int32_t E, int32_t N, int32_t n);
+sq_status sq_grouped_linear(const sq_packed_weight *stack, int32_t E, int32_t N, const int8_t *xq,
+                            const float *sx, const float *x_out, const int32_t *idx, int32_t n_out,
+                            int32_t rows, const int32_t *order, int32_t div, const int32_t *offsets,
+                            int32_t n, float *y, void *workspace, size_t ws_bytes,
+                            int32_t *dev_status, uint32_t flags, void *stream);
+
+/*
  * The experts' rows back to their tokens:
  *   out[t][:] = base[t][:] + sum_j gates[t][j] * z[place[t][j]][:]
  *   z      [rows][N] f32: the rows of sq_grouped_linear, in place order

@@ -66,3 +66,49 @@ def test_binding_refuses_cpu_tensors_and_wrong_types(L):
                  lambda: sq.combine(torch.zeros(4, 8), torch.zeros(2, 2), torch.zeros(2, 2, dtype=torch.int32))):
         with pytest.raises(sq.SQError):
             call()
+
+
+def _stack(L, E=4, N=30, K=300, mask=0, layout=1):
+    v = sq.SqPackedWeight()
+    assert L.sq_packed_view(ctypes.c_void_p(1 << 40), E * sq.round_up(N, 16), K, 128, mask, layout, ctypes.byref(v)) == 0
+    return v
+
+
+@pytest.mark.parametrize("mask", [0, 1])
+@pytest.mark.parametrize("layout", [sq.SQ_LAYOUT_TILES, sq.SQ_LAYOUT_TILES_ASYM])
+def test_expert_view(L, mask, layout):
+    v, e = _stack(L, mask=mask, layout=layout), sq.SqPackedWeight()
+    assert L.sq_expert_view(ctypes.byref(v), 4, 30, 3, ctypes.byref(e)) == 0
+    assert (e.N, e.K, e.layout, e.res_stride) == (30, 300, layout, 384)
+    assert e.res_q - v.res_q == 96 * 384 and e.sign_bits - v.sign_bits == 96 * 12 * 4
+    assert e.alpha - v.alpha == 96 * 4 and e.res_scale - v.res_scale == 96 * 3 * 4
+    assert (e.mask_bits is None) == (mask == 0)
+    if mask:
+        assert e.mask_bits - v.mask_bits == 96 * 12 * 4
+    if layout == sq.SQ_LAYOUT_TILES_ASYM:
+        assert e.res_zero - v.res_zero == 96 * 3 * 4
+    for args in ((4, 30, 4), (4, 30, -1)):
+        assert L.sq_expert_view(ctypes.byref(v), *args, ctypes.byref(e)) == 1
+    for args in ((4, 33, 0), (3, 30, 0), (0, 30, 0), (1025, 30, 0)):
+        assert L.sq_expert_view(ctypes.byref(v), *args, ctypes.byref(e)) == 2
+    rows, sparse = _stack(L, layout=0), _stack(L, layout=2)
+    for w in (rows, sparse):
+        assert L.sq_expert_view(ctypes.byref(w), 4, 30, 0, ctypes.byref(e)) == 1
+
+
+def test_grouped_linear_refusals(L):
+    v = _stack(L)
+
+    def call(stack=v, E=4, N=30, xq=P, sx=P, xo=P, idx=P, n_out=2, rows=8, order=P, div=2, off=P, n=16, y=P, ws=P,
+             wn=1 << 30, flags=0):
+        return L.sq_grouped_linear(None if stack is None else ctypes.byref(stack), E, N, xq, sx, xo, idx, n_out, rows,
+                                   order, div, off, n, y, ws, wn, None, flags, None)
+    assert call(stack=None) == 1 and call(stack=_stack(L, layout=0)) == 1 and call(stack=_stack(L, layout=2)) == 1
+    for name in ("xq", "sx", "xo", "idx", "off", "y"):
+        assert call(**{name: None}) == 1, name
+        assert call(**{name: BAD}) == 3, name
+    assert call(order=BAD) == 3 and call(ws=BAD) == 3
+    for kw in (dict(E=3), dict(N=33), dict(rows=0), dict(n=0), dict(div=0), dict(n_out=-1), dict(n_out=301),
+               dict(n=(1 << 24) + 1)):
+        assert call(**kw) == 2, kw
+    assert call(flags=2) == 1
