@@ -29,6 +29,9 @@ SQ_LAYOUT_TILES_SPARSE = 2
 SQ_LAYOUT_TILES_ASYM = 3
 SQ_GATE_TOPK = 0
 SQ_GATE_ALL = 1
+SQ_TYPE_F32 = 0
+SQ_TYPE_F16 = 1
+SQ_TYPE_BF16 = 2
 
 STATUS = {
     0: "SQ_OK", 1: "SQ_ERR_INVALID_ARG", 2: "SQ_ERR_SHAPE", 3: "SQ_ERR_ALIGN",
@@ -65,6 +68,14 @@ class SqNvfp4Matrix(ctypes.Structure):
     ]
 
 
+class SqLoraBank(ctypes.Structure):
+    _fields_ = [
+        ("S", ctypes.c_int32), ("R", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+        ("type", ctypes.c_int32), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p), ("rank", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -80,6 +91,8 @@ def lib():
     vp, i32, u32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t
     pw = ctypes.POINTER(SqPackedWeight)
     nm = ctypes.POINTER(SqNvfp4Matrix)
+    lb = ctypes.POINTER(SqLoraBank)
+    i64 = ctypes.c_int64
     sig = {
         "sq_nvfp4_bytes": ([i32, i32, i32], sz),
         "sq_nvfp4_view": ([vp, i32, i32, i32, nm], ctypes.c_int),
@@ -116,6 +129,8 @@ def lib():
         "sq_grouped_linear_workspace_bytes": ([pw, i32, i32, i32], sz),
         "sq_grouped_linear": ([pw, i32, i32, vp, vp, vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, sz, vp, u32, vp],
                               ctypes.c_int),
+        "sq_lora_workspace_bytes": ([lb, i32], sz),
+        "sq_lora_add": ([lb, vp, i32, vp, vp, vp, vp, i64, vp, i64, vp, sz, vp, u32, vp], ctypes.c_int),
         "sq_combine": ([vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, u32, vp], ctypes.c_int),
         "sq_testing_prefill_stalled": ([pw, vp, vp, vp, vp, i32, i32, vp, i32, ctypes.c_uint64, vp,
                                         vp], ctypes.c_int),
@@ -775,6 +790,81 @@ def combine(z, gates, place, base=None, out=None, status=None, pdl: bool = False
     _ck(lib().sq_combine(zp, rows, gp, pp, T, k, N, bp, op, _status_arg(status, w), _flags(pdl),
                          _stream(stream)), w)
     return out
+
+
+class LoraBank:
+    """S low-rank adapters of one projection: A [S][R][K], B [S][N][R] (float32,
+    float16 or bfloat16), scale [S] float32, rank [S] int32 (None: all R).  The
+    tensors are used in place: write an adapter's rows to load or replace it."""
+
+    def __init__(self, A, B, scale, rank=None):
+        import torch
+        w = "LoraBank"
+        types = {torch.float32: SQ_TYPE_F32, torch.float16: SQ_TYPE_F16, torch.bfloat16: SQ_TYPE_BF16}
+        if A.dim() != 3 or B.dim() != 3 or A.dtype not in types:
+            _refuse(w, "A must be [S][R][K] and B [S][N][R], float32, float16 or bfloat16")
+        self.S, self.R, self.K = A.shape
+        self.N = B.shape[1]
+        v = SqLoraBank(S=self.S, R=self.R, K=self.K, N=self.N, type=types[A.dtype])
+        v.A = _arg(A, A.dtype, (self.S, self.R, self.K), w, "A")
+        v.B = _arg(B, A.dtype, (self.S, self.N, self.R), w, "B")
+        v.scale = _arg(scale, torch.float32, (self.S,), w, "scale")
+        v.rank = _opt(rank, torch.int32, (self.S,), w, "rank")
+        self.view, self.A, self.B, self.scale, self.rank = v, A, B, scale, rank
+
+
+def lora_workspace_bytes(bank: LoraBank, M: int) -> int:
+    return int(lib().sq_lora_workspace_bytes(ctypes.byref(bank.view), M))
+
+
+def new_lora_workspace(bank: LoraBank, M: int, device=None):
+    """A workspace for lora_add over M tokens (one per call that may overlap
+    another)."""
+    import torch
+    return torch.empty(max(lora_workspace_bytes(bank, M), 16), dtype=torch.uint8, device=device or bank.A.device)
+
+
+def _rows_arg(t, shape, where: str, name: str):
+    """(address, row stride) of a float32 CUDA matrix with unit column stride."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or not t.is_cuda or t.dim() != 2:
+        _refuse(where, f"{name} must be a float32 CUDA matrix")
+    if tuple(t.shape) != shape:
+        _refuse(where, f"{name} must be {list(shape)}, got {list(t.shape)}", "SQ_ERR_SHAPE")
+    if (t.stride(1) != 1 and shape[1] > 1) or (shape[0] > 1 and t.stride(0) < shape[1]):
+        _refuse(where, f"{name} must have unit column stride and rows that do not overlap")
+    if t.get_device() != torch.cuda.current_device():
+        _refuse(where, f"{name} is not on the current device")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else max(shape[1], 1)
+
+
+def lora_add(bank: LoraBank, x, ids, base=None, y=None, segments: Segments = None, workspace=None, status=None,
+             pdl: bool = False, stream=None):
+    """y [M][N] = base + scale_a B_a (A_a x), a = ids[t] (int32, -1: no adapter).
+    base and y may be column slices of wider matrices, and the same one (in
+    place).  segments: segment(ids, bank.S), kept for the projections of a step."""
+    import torch
+    w = "sq_lora_add"
+    if x.dim() != 2:
+        _refuse(w, "x must be [M][K]", "SQ_ERR_SHAPE")
+    M, N = x.shape[0], bank.N
+    xp = _arg(x, torch.float32, (M, bank.K), w, "x")
+    ip = _arg(ids, torch.int32, (M,), w, "ids")
+    if y is None:
+        y = torch.empty(M, N, dtype=torch.float32, device=x.device)
+    yp, ldy = _rows_arg(y, (M, N), w, "y")
+    bp, ldb = (None, N) if base is None else _rows_arg(base, (M, N), w, "base")
+    fp = op = None
+    if segments is not None:
+        fp = _arg(segments.offsets, torch.int32, (bank.S + 1,), w, "segments.offsets")
+        op = _arg(segments.order, torch.int32, (M,), w, "segments.order")
+    if workspace is None:
+        workspace, wp, wn = _workspace_arg(None, lora_workspace_bytes(bank, M), x.device, w)
+    else:
+        wp, wn = _arg(workspace, torch.uint8, (workspace.numel(),), w, "workspace"), workspace.numel()
+    _ck(lib().sq_lora_add(ctypes.byref(bank.view), xp, M, ip, fp, op, bp, ldb, yp, ldy, wp, wn,
+                          _status_arg(status, w), _flags(pdl), _stream(stream)), w)
+    return y
 
 
 def testing_read_peak(buf, iters: int = 20, stream=None) -> float:

@@ -763,6 +763,45 @@ sq_status sq_combine(const float* z, int32_t rows, const float* gates, const int
                                   static_cast<cudaStream_t>(stream)));
 }
 
+static sq_status check_bank(const sq_lora_bank* b) {
+  if (!b || !b->A || !b->B || !b->scale) return SQ_ERR_INVALID_ARG;
+  if (b->type != SQ_TYPE_F32 && b->type != SQ_TYPE_F16 && b->type != SQ_TYPE_BF16) return SQ_ERR_INVALID_ARG;
+  if (b->S < 1 || b->S > kMaxSegments || b->R < 1 || b->R > kMaxLoraRank || b->K < 1 || b->K > kMaxLoraK || b->N < 1 ||
+      b->N > (1 << 24))
+    return SQ_ERR_SHAPE;
+  if (!aligned16(b->A) || !aligned16(b->B) || !aligned16(b->scale) || (b->rank && !aligned16(b->rank)))
+    return SQ_ERR_ALIGN;
+  return SQ_OK;
+}
+
+static constexpr int32_t kMaxLoraTokens = 1 << 20;
+
+size_t sq_lora_workspace_bytes(const sq_lora_bank* bank, int32_t M) {
+  if (check_bank(bank) != SQ_OK || M < 1 || M > kMaxLoraTokens) return 0;
+  return lora_workspace_bytes(M, bank->S, bank->R);
+}
+
+sq_status sq_lora_add(const sq_lora_bank* bank, const float* x, int32_t M, const int32_t* ids, const int32_t* offsets,
+                      const int32_t* order, const float* base, int64_t ld_base, float* y, int64_t ld_y, void* workspace,
+                      size_t ws_bytes, int32_t* dev_status, uint32_t flags, void* stream) {
+  sq_status st = check_bank(bank);
+  if (st != SQ_OK) return st;
+  if (!x || !ids || !y || (offsets == nullptr) != (order == nullptr)) return SQ_ERR_INVALID_ARG;
+  if (M < 1 || M > kMaxLoraTokens || ld_y < bank->N || (base && ld_base < bank->N) || ld_y > (1ll << 32) ||
+      (base && ld_base > (1ll << 32)))
+    return SQ_ERR_SHAPE;
+  if ((base == y && ld_base != ld_y) || (flags & ~SQ_LAUNCH_PDL)) return SQ_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(ids) || (offsets && (!aligned16(offsets) || !aligned16(order))) ||
+      (workspace && !aligned16(workspace)) || ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(y)) & 3u))
+    return SQ_ERR_ALIGN;
+  const size_t need = lora_workspace_bytes(M, bank->S, bank->R);
+  if (need && (!workspace || ws_bytes < need)) return SQ_ERR_WORKSPACE;
+  DeviceInfo d;
+  if ((st = check_device(&d)) != SQ_OK) return st;
+  return from_cuda(launch_lora(*bank, x, M, ids, offsets, order, base, ld_base, y, ld_y, workspace, dev_status,
+                               (flags & SQ_LAUNCH_PDL) != 0, d.sm_count, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"
 
 // ---- failure injection for the tests (include/sq_testing.h) -----------------------

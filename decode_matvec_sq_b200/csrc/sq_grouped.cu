@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
     pdl_wait();
     pdl_launch_dependents();
   }
-  const int groups = segment_units<kThreads>(a, TG, pre, part_i);
+  const int groups = segment_units<kThreads>(a.offsets, a.E, a.n, a.status, TG, pre, part_i);
 
   // the CTA's (group, row block) pairs: the fewest CTAs with the largest share
   // that one CTA per SM gives
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
   auto enter = [&](int64_t v, bool new_group) {
     if (new_group) {
       const int u = (int)(v / a.rbe), e = unit_expert(pre, a.E, u);
-      const int2 b = segment_bounds(a, e);
+      const int2 b = segment_bounds(a.offsets, a.n, e, a.status);
       const int p0 = b.x + (u - pre[e]) * TG;
       load_tokens<NT>(tk, a, p0, min(TG, b.y - p0), gid, tid4);
       rb = (int)(v - (int64_t)u * a.rbe);

@@ -36,12 +36,12 @@ struct GroupedArgs {
   int pdl;
 };
 
-// Bounds of segment e, clamped to the n places (offsets that do not ascend in
-// [0, n] are reported; no access leaves the arrays).
-__device__ __forceinline__ int2 segment_bounds(const GroupedArgs& p, int e) {
-  const int a = __ldg(p.offsets + e), b = __ldg(p.offsets + e + 1);
-  const int ca = min(max(a, 0), p.n), cb = min(max(b, ca), p.n);
-  if (ca != a || cb != b) set_status(p.status, SQ_ERR_INVALID_ARG);
+// Bounds of segment e of a sort of n entries, clamped to them (offsets that do
+// not ascend in [0, n] are reported; no access leaves the arrays).
+__device__ __forceinline__ int2 segment_bounds(const int32_t* offsets, int n, int e, int32_t* status) {
+  const int a = __ldg(offsets + e), b = __ldg(offsets + e + 1);
+  const int ca = min(max(a, 0), n), cb = min(max(b, ca), n);
+  if (ca != a || cb != b) set_status(status, SQ_ERR_INVALID_ARG);
   return make_int2(ca, cb);
 }
 
@@ -63,14 +63,14 @@ __device__ __forceinline__ int source_row(const GroupedArgs& p, int at) {
 // Exclusive sums over the experts of ceil(segment / unit), into pre[0 .. E]
 // (shared memory; all threads of the CTA call it; part: one int per warp).
 template <int THREADS>
-__device__ int segment_units(const GroupedArgs& p, int unit, int* pre, int* part) {
+__device__ int segment_units(const int32_t* offsets, int E, int n, int32_t* status, int unit, int* pre, int* part) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int carry = 0;
-  for (int e0 = 0; e0 < p.E; e0 += THREADS) {
+  for (int e0 = 0; e0 < E; e0 += THREADS) {
     const int e = e0 + (int)threadIdx.x;
     int v = 0;
-    if (e < p.E) {
-      const int2 b = segment_bounds(p, e);
+    if (e < E) {
+      const int2 b = segment_bounds(offsets, n, e, status);
       v = (b.y - b.x + unit - 1) / unit;
     }
     int incl = v;
@@ -86,11 +86,11 @@ __device__ int segment_units(const GroupedArgs& p, int unit, int* pre, int* part
       if (w < warp) before += part[w];
       total += part[w];
     }
-    if (e < p.E) pre[e] = before + incl - v;
+    if (e < E) pre[e] = before + incl - v;
     carry = total;
     __syncthreads();
   }
-  if (threadIdx.x == 0) pre[p.E] = carry;
+  if (threadIdx.x == 0) pre[E] = carry;
   __syncthreads();
   return carry;
 }

@@ -137,4 +137,15 @@ struct GroupedArgs;
 size_t grouped_workspace_bytes(int E, int N, int K, int64_t n);
 cudaError_t launch_grouped(const GroupedArgs& a, void* workspace, int sm_count, cudaStream_t stream);
 
+// Low-rank adapters (sq_lora.cu).  Up to kLoraDecodeTokens tokens take one
+// launch and no workspace.
+constexpr int kLoraDecodeTokens = 64;
+constexpr int kMaxLoraRank = 256;
+constexpr int kMaxLoraK = 65536;
+size_t lora_workspace_bytes(int M, int S, int R);
+cudaError_t launch_lora(const sq_lora_bank& bank, const float* x, int M, const int32_t* ids,
+                        const int32_t* offsets, const int32_t* order, const float* base, int64_t ldb,
+                        float* y, int64_t ldy, void* workspace, int32_t* status, bool pdl,
+                        int sm_count, cudaStream_t stream);
+
 }  // namespace sq

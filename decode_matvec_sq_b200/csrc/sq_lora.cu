@@ -1,0 +1,757 @@
+// sq_lora.cu -- low-rank adapters of many requests at once, beside a shared
+// projection (sm_100a):
+//
+//   y[t] = base[t] + scale_a B_a (A_a x_t),   a = ids[t],
+//
+// A_a [rank_a][K], B_a [N][rank_a] in binary32, binary16 or bfloat16, x, base and
+// y in binary32, every product and sum in binary32 or better.
+//
+// Few tokens (a decode step): one launch.  A cluster of kCluster CTAs serves up
+// to kGroup tokens that share an adapter (found from the ids by ballots): each CTA
+// forms its channels' part of v = A x on the CUDA cores, the parts meet over
+// distributed shared memory, and each CTA adds its columns of B v.  The adapter
+// is read once, by the cluster, and there is no second launch to wait for.
+//
+// More tokens: the tokens are sorted by adapter and cut into tiles of 64, and two
+// tensor-core kernels (mma.sync) follow.  Shrink: a tile is a cluster, its CTAs
+// and warps split the channels; the parts are summed over distributed shared
+// memory in a fixed order.  Expand: a warp holds 16 tokens' v as MMA operands
+// and streams over the columns.  Both are bound by memory (x once; base and y
+// once): the products have a few dozen terms per byte.
+// Precision: the tensor cores take 16-bit operands, so a binary32 value is cut
+// into three bfloat16 parts that sum to it exactly (8 significand bits each, by
+// truncation) and the products of parts are summed in binary32; of two cut
+// operands the products below 2^-24 are left out.  A binary16 weight is two
+// bfloat16 parts exactly.  In the expand kernel a binary16 weight is taken as it
+// is, and v, scaled by a power of two per token into binary16's range, as two
+// binary16 parts (rounded: 2^-23 of v).
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "sq_grouped.cuh"
+#include "sq_internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace sq {
+namespace {
+
+constexpr int kCluster = 8;        // CTAs per cluster (the portable size)
+constexpr int kDecodeThreads = 256;
+constexpr int kGroup = 4;          // tokens per cluster of the decode kernel
+constexpr int kTile = 64;          // tokens per tile of the two-kernel route
+constexpr int kExpandCols = 256;   // columns of y per piece of the decode expand
+
+struct Params {
+  const void* A;
+  const void* B;
+  const float* scale;
+  const int32_t* rank;
+  int S, R, K, N;
+  const float* x;
+  int M;
+  const int32_t* ids;
+  const float* base;
+  int64_t ldb;
+  float* y;
+  int64_t ldy;
+  const int32_t* offsets;
+  const int32_t* order;
+  float* v;   // [M][Rp], in place order
+  int Rp;     // R rounded up to 32
+  int32_t* status;
+  int pdl;
+  int span;   // expand: columns per CTA
+  int tiles;  // expand: CTAs along the tiles (the rest copy rows without adapter)
+};
+
+__device__ __forceinline__ int adapter_rank(const Params& p, int a) {
+  return p.rank ? min(max(__ldg(p.rank + a), 0), p.R) : p.R;
+}
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Eight consecutive elements from an address aligned to them.
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// Elements i0 .. i0 + 7 of a row of `len` live elements (the rest 0, not read);
+// VEC: rows start at addresses that allow load8.
+template <bool VEC, class W>
+__device__ __forceinline__ void load_row8(const W* row, int i0, int len, float (&v)[8]) {
+  if (VEC && i0 + 8 <= len) {
+    load8(row + i0, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i0 + i < len ? to_f(row[i0 + i]) : 0.0f;
+  }
+}
+
+// ---- few tokens: one launch -------------------------------------------------------
+
+template <class W, bool VECK, bool VECR>
+__global__ void __launch_bounds__(kDecodeThreads) k_lora_decode(const Params p) {
+  extern __shared__ __align__(16) float sm[];
+  __shared__ int members[kGroup], n_members, adapter;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int c = (int)cluster.block_rank(), t = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kWarps = kDecodeThreads / 32;
+  if (p.pdl) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+  // the tokens of t's adapter: this cluster serves t and the next of them if
+  // kGroup divides the number of them before t
+  if (warp == 0) {
+    const int a = __ldg(p.ids + t);
+    const bool ok = a >= 0 && a < p.S;
+    if (!ok && a != -1 && lane == 0) set_status(p.status, SQ_ERR_INVALID_ARG);
+    int before = 0, found = 0;
+    for (int u0 = 0; u0 < p.M; u0 += 32) {
+      const int u = u0 + lane;
+      const uint32_t same = __ballot_sync(0xffffffffu, ok && u < p.M && __ldg(p.ids + u) == a);
+      const uint32_t past = u0 > t ? 0xffffffffu : t - u0 >= 32 ? 0u : 0xffffffffu << (t - u0);
+      before += __popc(same & ~past);
+      const int at = found + __popc(same & past & ((1u << lane) - 1u));
+      if (((same & past) >> lane & 1u) && at < kGroup) members[at] = u;
+      found += __popc(same & past);
+    }
+    if (lane == 0) {
+      adapter = ok ? a : -1;
+      n_members = !ok ? 0 : before % kGroup == 0 ? min(found, kGroup) : -1;
+    }
+  }
+  __syncthreads();
+  const int nm = n_members, a = adapter;
+  const int n0 = (int)((int64_t)p.N * c / kCluster), n1 = (int)((int64_t)p.N * (c + 1) / kCluster);
+  if (nm <= 0) {  // no adapter (nm = 0: the base row as it is), or served by another cluster
+    if (nm == 0 && p.base != p.y)
+      for (int n = n0 + threadIdx.x; n < n1; n += kDecodeThreads)
+        p.y[t * p.ldy + n] = p.base ? p.base[t * p.ldb + n] : 0.0f;
+    return;  // (the whole cluster)
+  }
+  const int rank = adapter_rank(p, a);
+  // this CTA's channels, in units of 8
+  const int k8 = (p.K + 7) / 8;
+  const int k0 = (int)((int64_t)k8 * c / kCluster) * 8, k1 = min(p.K, (int)((int64_t)k8 * (c + 1) / kCluster) * 8);
+  const int ks = ((k8 + kCluster - 1) / kCluster) * 8;  // row stride of the x slice
+  float* xs = sm;                        // [kGroup][ks]
+  float* vp = xs + kGroup * ks;          // [kGroup][R]: this CTA's part of v
+  float* vs = vp + kGroup * p.R;         // [kGroup][R rounded up to 8]: v
+  const int Rv = (p.R + 7) & ~7;
+  float* out = vs + kGroup * Rv;         // [kGroup][kExpandCols]
+  for (int i = threadIdx.x; i < kGroup * ks; i += kDecodeThreads) {
+    const int g = i / ks, k = k0 + i % ks;
+    xs[i] = g < nm && k < k1 ? __ldg(p.x + (int64_t)members[g] * p.K + k) : 0.0f;
+  }
+  __syncthreads();
+  const W* Aa = static_cast<const W*>(p.A) + (int64_t)a * p.R * p.K + k0;
+  const int len = max(0, k1 - k0);
+  for (int r0 = warp * 4; r0 < rank; r0 += kWarps * 4) {
+    float acc[4][kGroup] = {};
+    for (int i0 = lane * 8; i0 < len; i0 += 256) {
+      float w[4][8];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool live = r0 + r < rank;
+        load_row8<VECK>(Aa + (int64_t)(live ? r0 + r : r0) * p.K, i0, live ? len : 0, w[r]);
+      }
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g) {
+        const float4 x0 = *reinterpret_cast<const float4*>(xs + g * ks + i0);
+        const float4 x1 = *reinterpret_cast<const float4*>(xs + g * ks + i0 + 4);
+        const float xv[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[r][g] = fmaf(w[r][i], xv[i], acc[r][g]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) acc[r][g] += __shfl_xor_sync(0xffffffffu, acc[r][g], o);
+        if (lane == 0 && r0 + r < rank) vp[g * p.R + r0 + r] = acc[r][g];
+      }
+  }
+  cluster.sync();
+  bool bad = false;
+  const float sc = __ldg(p.scale + a);
+  for (int i = threadIdx.x; i < kGroup * Rv; i += kDecodeThreads) {
+    const int g = i / Rv, r = i % Rv;
+    float v = 0.0f;
+    if (g < nm && r < rank) {
+#pragma unroll
+      for (int d = 0; d < kCluster; ++d) v += *cluster.map_shared_rank(vp + g * p.R + r, d);
+      bad |= !isfinite(v);
+      v *= sc;
+    }
+    vs[i] = v;
+  }
+  if (bad) set_status(p.status, SQ_ERR_NONFINITE);
+  // the parts have been read: no CTA leaves before every other has got here
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  __syncthreads();
+  const W* Ba = static_cast<const W*>(p.B) + (int64_t)a * p.N * p.R;
+  const int nv = (rank + 7) / 8;                       // vectors of 8 per row of B
+  int lpr = 1;                                         // lanes per row: a power of two <= nv
+  while (lpr * 2 <= nv && lpr < 32) lpr *= 2;
+  const int sub = lane & (lpr - 1), rpw = 32 / lpr;    // rows per warp pass
+  for (int c0 = n0; c0 < n1; c0 += kExpandCols) {
+    const int cols = min(kExpandCols, n1 - c0);
+    // (every lane of a warp takes the same number of passes)
+    for (int b0 = warp * rpw; b0 < cols; b0 += kWarps * rpw) {
+      const int n = b0 + lane / lpr;
+      float acc[kGroup] = {};
+      for (int j = sub; j < nv; j += lpr) {
+        float w[8];
+        load_row8<VECR>(Ba + (int64_t)(c0 + min(n, cols - 1)) * p.R, 8 * j, rank, w);
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) {
+          const float4 x0 = *reinterpret_cast<const float4*>(vs + g * Rv + 8 * j);
+          const float4 x1 = *reinterpret_cast<const float4*>(vs + g * Rv + 8 * j + 4);
+          const float xv[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[g] = fmaf(w[i], xv[i], acc[g]);
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g) {
+        for (int o = lpr >> 1; o > 0; o >>= 1) acc[g] += __shfl_xor_sync(0xffffffffu, acc[g], o);
+        if (sub == 0 && n < cols) out[g * kExpandCols + n] = acc[g];
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nm * kExpandCols; i += kDecodeThreads) {
+      const int g = i / kExpandCols, n = i % kExpandCols;
+      if (n < cols) {
+        const int64_t row = members[g];
+        const float b = p.base ? p.base[row * p.ldb + c0 + n] : 0.0f;
+        p.y[row * p.ldy + c0 + n] = b + out[i];
+      }
+    }
+    __syncthreads();
+  }
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// ---- many tokens: tensor cores ---------------------------------------------------------
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Upper halves of two binary32 values as a pair of bfloat16 (first in the low half).
+__device__ __forceinline__ uint32_t upper_pair(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ float below_upper(float v) { return v - __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
+
+// Eight values as T bfloat16 parts (by truncation; T = 3 is exact for binary32,
+// T = 2 for binary16), four pairs each.
+template <int T>
+__device__ __forceinline__ void cut8(float (&v)[8], uint32_t (&o)[T][4]) {
+#pragma unroll
+  for (int s = 0; s < T; ++s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[s][i] = upper_pair(v[2 * i], v[2 * i + 1]);
+    if (s + 1 < T) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = below_upper(v[i]);
+    }
+  }
+}
+
+template <class W>
+struct Parts;  // bfloat16 parts of a weight
+template <>
+struct Parts<__nv_bfloat16> { static constexpr int n = 1; };
+template <>
+struct Parts<__half> { static constexpr int n = 2; };
+template <>
+struct Parts<float> { static constexpr int n = 3; };
+
+// Elements i0 .. i0 + 7 of a weight row (`len` live) as bfloat16 parts.
+template <bool VEC, class W>
+__device__ __forceinline__ void weight_parts(const W* row, int i0, int len, uint32_t (&o)[Parts<W>::n][4]) {
+  if constexpr (std::is_same<W, __nv_bfloat16>::value && VEC) {
+    if (i0 + 8 <= len) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(row + i0));
+      o[0][0] = a.x; o[0][1] = a.y; o[0][2] = a.z; o[0][3] = a.w;
+      return;
+    }
+  }
+  float v[8];
+  load_row8<VEC>(row, i0, len, v);
+  cut8<Parts<W>::n>(v, o);
+}
+
+// The MMA's k index is free as long as both operands agree: over 32 channels lane
+// tid4 holds channels 8 tid4 .. 8 tid4 + 7, the first four in one k16 step and the
+// last four in the next, so that every load is 16 bytes or more of a row.
+// Shrink: cluster = one tile of 64 tokens of one adapter; CTA c, warp half h take
+// slice 2c + h of the channels, warp pair (w % 4) the tokens 16 (w % 4) ...
+constexpr int kShrinkThreads = 256;
+constexpr int kSlices = 2 * kCluster;
+
+template <class W, bool VEC, int NT>
+__global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) {
+  extern __shared__ __align__(16) float sm[];  // [2 halves][kTile][Rp], then the tile sums [S + 1]
+  __shared__ int part_i[kShrinkThreads / 32];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int c = (int)cluster.block_rank(), u = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tid4 = lane & 3;
+  int* pre = reinterpret_cast<int*>(sm + 2 * kTile * p.Rp);
+  pdl_wait();
+  pdl_launch_dependents();
+  const int units = segment_units<kShrinkThreads>(p.offsets, p.S, p.M, p.status, kTile, pre, part_i);
+  if (u >= units) return;  // (the whole cluster)
+  const int a = unit_expert(pre, p.S, u);
+  const int2 seg = segment_bounds(p.offsets, p.M, a, p.status);
+  const int p0 = seg.x + (u - pre[a]) * kTile, cnt = min(kTile, seg.y - p0);
+  const int rank = adapter_rank(p, a);
+  const int tg = warp & 3, half = warp >> 2, first = 16 * tg;
+  const int steps = (p.K + 31) / 32, slice = 2 * c + half;
+  const int s0 = (int)((int64_t)steps * slice / kSlices), s1 = (int)((int64_t)steps * (slice + 1) / kSlices);
+  float* mine = sm + half * kTile * p.Rp;
+  if (first < cnt) {
+    const float* xr[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      int t = __ldg(p.order + p0 + min(first + gid + 8 * h, cnt - 1));
+      if (t < 0 || t >= p.M) {
+        set_status(p.status, SQ_ERR_INVALID_ARG);
+        t = 0;
+      }
+      xr[h] = p.x + (int64_t)t * p.K;
+    }
+    const W* Aa = static_cast<const W*>(p.A) + (int64_t)a * p.R * p.K;
+    for (int r0 = 0; r0 < p.Rp; r0 += 8 * NT) {  // (one pass up to rank 8 NT)
+      float acc[NT][4] = {};
+      if (r0 < rank) {
+#pragma unroll 2
+        for (int s = s0; s < s1; ++s) {
+          const int k = 32 * s + 8 * tid4;
+          uint32_t xa[2][3][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v[8];
+            load_row8<VEC>(xr[h], k, p.K, v);
+            cut8<3>(v, xa[h]);
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const int r = r0 + 8 * j + gid;
+            if (r0 + 8 * j >= rank) break;
+            uint32_t w[Parts<W>::n][4];
+            weight_parts<VEC>(Aa + (int64_t)min(r, rank - 1) * p.K, k, r < rank ? p.K : 0, w);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int i = 2; i >= 0; --i) {  // small products first
+                const uint32_t av[4] = {xa[0][i][2 * q], xa[1][i][2 * q], xa[0][i][2 * q + 1], xa[1][i][2 * q + 1]};
+#pragma unroll
+                for (int m = Parts<W>::n - 1; m >= 0; --m)
+                  if (i + m < 3) mma_bf16(acc[j], av, w[m][2 * q], w[m][2 * q + 1]);
+              }
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        if (r0 + 8 * j < p.Rp) {
+          float* o = mine + (first + gid) * p.Rp + r0 + 8 * j + 2 * tid4;
+          *reinterpret_cast<float2*>(o) = make_float2(acc[j][0], acc[j][1]);
+          *reinterpret_cast<float2*>(o + 8 * p.Rp) = make_float2(acc[j][2], acc[j][3]);
+        }
+    }
+  }
+  cluster.sync();
+  // CTA c sums its eighth of the tile's values over the slices, in order
+  const int total = cnt * p.Rp, i0 = (int)((int64_t)total * c / kCluster), i1 = (int)((int64_t)total * (c + 1) / kCluster);
+  const float sc = __ldg(p.scale + a);
+  bool bad = false;
+  for (int i = i0 + threadIdx.x; i < i1; i += kShrinkThreads) {
+    float v = 0.0f;
+#pragma unroll
+    for (int d = 0; d < kCluster; ++d) {
+      const float* o = cluster.map_shared_rank(sm, d);
+      v += o[i] + o[kTile * p.Rp + i];
+    }
+    bad |= !isfinite(v);
+    p.v[(int64_t)p0 * p.Rp + i] = v * sc;
+  }
+  if (bad) set_status(p.status, SQ_ERR_NONFINITE);
+  cluster.sync();  // no CTA leaves while its parts may be read
+}
+
+constexpr int kExpandThreads = 128;
+constexpr int kBlockCols = 64;  // columns of y per warp pass
+
+// Operands of v in the expand kernel: three bfloat16 parts, or two binary16 parts.
+template <class W>
+constexpr int kVParts = std::is_same<W, __half>::value ? 2 : 3;
+
+// Expand: CTA = one tile of 64 tokens (16 per warp) and a span of columns.  The
+// warp's v lies in shared memory in operand order ([k32 step][part][two 16-byte
+// words per lane]).  Of each 16 columns, one MMA takes columns 4i, 4i+1 and one
+// 4i+2, 4i+3 (i = 0..3), so that a lane's accumulators are four neighbouring
+// columns and base and y move in 16-byte words.
+template <class W, bool VEC, bool VECY>
+__global__ void __launch_bounds__(kExpandThreads) k_lora_expand(const Params p) {
+  constexpr int NV = kVParts<W>;
+  constexpr bool HALF = NV == 2;
+  extern __shared__ __align__(16) uint4 vsm[];  // [4 warps][Rp / 32][NV][2][32], then the tile sums
+  __shared__ int part_i[kExpandThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tid4 = lane & 3;
+  const int u = blockIdx.y;
+  const int n0 = blockIdx.x * p.span, n1 = min(p.N, n0 + p.span);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (u >= p.tiles) {  // rows without an adapter
+    if (p.base == p.y) return;
+    for (int t = (u - p.tiles) * 4 + warp; t < p.M; t += ((int)gridDim.y - p.tiles) * 4) {
+      const int a = __ldg(p.ids + t);
+      if (a >= 0 && a < p.S) continue;
+      for (int n = n0 + lane; n < n1; n += 32) p.y[t * p.ldy + n] = p.base ? p.base[t * p.ldb + n] : 0.0f;
+    }
+    return;
+  }
+  const int steps_all = p.Rp / 32;
+  int* pre = reinterpret_cast<int*>(vsm + 4 * steps_all * NV * 64);
+  const int units = segment_units<kExpandThreads>(p.offsets, p.S, p.M, p.status, kTile, pre, part_i);
+  if (u >= units) return;
+  const int a = unit_expert(pre, p.S, u);
+  const int2 seg = segment_bounds(p.offsets, p.M, a, p.status);
+  const int p0 = seg.x + (u - pre[a]) * kTile + 16 * warp, cnt = min(16, seg.y - p0);
+  if (cnt <= 0) return;  // (no barrier follows)
+  const int rank = adapter_rank(p, a), steps = (rank + 31) / 32;
+  uint4* vw = vsm + warp * steps_all * NV * 64;
+  float back[2] = {1.0f, 1.0f};  // binary16 parts: 2^e of the two rows
+  int64_t row[2];
+  const float* vrow[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int at = p0 + min(gid + 8 * h, cnt - 1);
+    int t = __ldg(p.order + at);
+    if (t < 0 || t >= p.M) t = 0;  // (reported by the shrink kernel)
+    row[h] = t;
+    vrow[h] = p.v + (int64_t)at * p.Rp;
+  }
+  float to[2] = {1.0f, 1.0f};
+  if constexpr (HALF) {
+    float m[2] = {0.0f, 0.0f};
+    for (int s = 0; s < steps; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float4 f = *reinterpret_cast<const float4*>(vrow[h] + 32 * s + 8 * tid4 + 4 * i);
+          m[h] = fmaxf(m[h], fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w))));
+        }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      m[h] = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], 1));
+      m[h] = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], 2));
+      // the largest |v| to [2^13, 2^14): exponent field of the power is 267 - its own,
+      // kept inside the normal range (a row of zeros or of tiny values stays below)
+      const int ex = (int)(__float_as_uint(m[h]) >> 23);
+      const int f = min(max(267 - ex, 1), 253);
+      to[h] = __uint_as_float((uint32_t)f << 23);
+      back[h] = __uint_as_float((uint32_t)(254 - f) << 23);
+    }
+  }
+  for (int s = 0; s < steps; ++s) {
+    uint32_t o[2][3][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 f = *reinterpret_cast<const float4*>(vrow[h] + 32 * s + 8 * tid4 + 4 * i);
+        v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+      }
+      if constexpr (HALF) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x0 = v[2 * i] * to[h], x1 = v[2 * i + 1] * to[h];
+          const __half2 hi = __floats2half2_rn(x0, x1);
+          const float2 hf = __half22float2(hi);
+          const __half2 lo = __floats2half2_rn(x0 - hf.x, x1 - hf.y);
+          o[h][0][i] = *reinterpret_cast<const uint32_t*>(&hi);
+          o[h][1][i] = *reinterpret_cast<const uint32_t*>(&lo);
+        }
+      } else {
+        cut8<3>(v, o[h]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        vw[((s * NV + i) * 2 + q) * 32 + lane] =
+            make_uint4(o[0][i][2 * q], o[1][i][2 * q], o[0][i][2 * q + 1], o[1][i][2 * q + 1]);
+  }
+  __syncwarp();
+  const W* Ba = static_cast<const W*>(p.B) + (int64_t)a * p.N * p.R;
+  const int col = 4 * (gid >> 1) + (gid & 1);  // this lane's B column of each 16 (and + 2)
+  for (int c0 = n0; c0 < n1; c0 += kBlockCols) {
+    // base first: its latency passes under the products
+    float b[4][2][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int n = c0 + 16 * j + 4 * tid4;
+        const bool live = gid + 8 * h < cnt && p.base != nullptr;
+        if (VECY && live && n + 4 <= n1) {
+          const float4 f = *reinterpret_cast<const float4*>(p.base + row[h] * p.ldb + n);
+          b[j][h][0] = f.x; b[j][h][1] = f.y; b[j][h][2] = f.z; b[j][h][3] = f.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) b[j][h][i] = live && n + i < n1 ? p.base[row[h] * p.ldb + n + i] : 0.0f;
+        }
+      }
+    float acc[8][4] = {};
+    for (int s = 0; s < steps; ++s) {
+      uint32_t va[NV][2][4];
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint4 f = vw[((s * NV + i) * 2 + q) * 32 + lane];
+          va[i][q][0] = f.x; va[i][q][1] = f.y; va[i][q][2] = f.z; va[i][q][3] = f.w;
+        }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int n = c0 + 16 * (j >> 1) + col + 2 * (j & 1);
+        const W* wr = Ba + (int64_t)min(n, n1 - 1) * p.R;
+        if constexpr (HALF) {
+          uint32_t w[4];
+          if (VEC && 32 * s + 8 * tid4 + 8 <= rank) {
+            const uint4 f = __ldg(reinterpret_cast<const uint4*>(wr + 32 * s + 8 * tid4));
+            w[0] = f.x; w[1] = f.y; w[2] = f.z; w[3] = f.w;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 32 * s + 8 * tid4 + 2 * i;
+              const __half2 f = __halves2half2(r < rank ? wr[r] : __float2half(0.0f),
+                                               r + 1 < rank ? wr[r + 1] : __float2half(0.0f));
+              w[i] = *reinterpret_cast<const uint32_t*>(&f);
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            mma_f16(acc[j], va[1][q], w[2 * q], w[2 * q + 1]);
+            mma_f16(acc[j], va[0][q], w[2 * q], w[2 * q + 1]);
+          }
+        } else {
+          uint32_t w[Parts<W>::n][4];
+          weight_parts<VEC>(wr, 32 * s + 8 * tid4, rank, w);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = NV - 1; i >= 0; --i)
+#pragma unroll
+              for (int m = Parts<W>::n - 1; m >= 0; --m)
+                if (i + m < 3) mma_bf16(acc[j], va[i][q], w[m][2 * q], w[m][2 * q + 1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (gid + 8 * h >= cnt) continue;
+        const int n = c0 + 16 * j + 4 * tid4;
+        float o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = fmaf(acc[2 * j + (i >> 1)][2 * h + (i & 1)], back[h], b[j][h][i]);
+        float* yr = p.y + row[h] * p.ldy + n;
+        if (VECY && n + 4 <= n1) {
+          *reinterpret_cast<float4*>(yr) = make_float4(o[0], o[1], o[2], o[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n + i < n1) yr[i] = o[i];
+        }
+      }
+  }
+}
+
+cudaError_t launch(void (*fn)(const Params), dim3 grid, int threads, int smem, int cluster, bool pdl, cudaStream_t stream,
+                   const Params& p) {
+  const cudaError_t e = ensure_smem_attr((const void*)fn, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+bool aligned(const void* q, int64_t stride_elems, int elem, int bytes) {
+  return reinterpret_cast<uintptr_t>(q) % bytes == 0 && stride_elems * elem % bytes == 0;
+}
+
+template <class W>
+cudaError_t launch_type(Params p, void* sort_ws, int32_t* sort_arrays, int sm_count, cudaStream_t stream) {
+  // rows of A and x (B) start at addresses that allow 8-element vectors
+  const bool veck = p.K % 8 == 0 && aligned(p.A, p.K, sizeof(W), 16) && aligned(p.x, p.K, 4, 16);
+  const bool vecr = aligned(p.B, p.R, sizeof(W), 16);
+  const bool pdl = p.pdl != 0;
+  if (p.M <= kLoraDecodeTokens) {
+    const int ks = (int)ceil_div(ceil_div(p.K, 8), kCluster) * 8;
+    const int smem = 4 * kGroup * (ks + p.R + (int)round_up(p.R, 8) + kExpandCols) + 16;
+    auto* fn = veck ? (vecr ? k_lora_decode<W, true, true> : k_lora_decode<W, true, false>)
+                    : (vecr ? k_lora_decode<W, false, true> : k_lora_decode<W, false, false>);
+    return launch(fn, dim3(kCluster, p.M), kDecodeThreads, smem, kCluster, pdl, stream, p);
+  }
+  if (!p.offsets) {
+    int32_t* offsets = sort_arrays;
+    int32_t* order = offsets + round_up(p.S + 1, 4);
+    int32_t* place = order + round_up(p.M, 4);
+    const cudaError_t e = launch_segment(p.ids, p.M, p.S, offsets, order, place, sort_ws, p.status, pdl, stream);
+    if (e != cudaSuccess) return e;
+    p.offsets = offsets;
+    p.order = order;
+  }
+  // tiles: at most one partial tile per adapter
+  const int tiles = (int)(p.M / kTile + std::min(p.S, p.M));
+  const int tables = (int)round_up(4 * (p.S + 1), 16);
+  {
+    const int smem = 2 * kTile * p.Rp * 4 + tables;
+    auto* fn = p.Rp <= 32 ? (veck ? k_lora_shrink<W, true, 4> : k_lora_shrink<W, false, 4>)
+                          : (veck ? k_lora_shrink<W, true, 8> : k_lora_shrink<W, false, 8>);
+    const cudaError_t e = launch(fn, dim3(kCluster, tiles), kShrinkThreads, smem, kCluster, true, stream, p);
+    if (e != cudaSuccess) return e;
+  }
+  // columns per CTA: a few CTAs per SM over all tiles
+  const int64_t live = ceil_div(p.M, kTile);
+  p.span = (int)std::max<int64_t>(kBlockCols, round_up(ceil_div((int64_t)p.N * live, 8 * (int64_t)sm_count), kBlockCols));
+  p.tiles = tiles;
+  const int copies = p.base == p.y ? 0 : (int)std::min<int64_t>(ceil_div(p.M, 64), 64);
+  const bool vecy = aligned(p.y, p.ldy, 4, 16) && (!p.base || aligned(p.base, p.ldb, 4, 16));
+  const int smem = 4 * (p.Rp / 32) * kVParts<W> * 64 * 16 + tables;
+  auto* fn = vecr ? (vecy ? k_lora_expand<W, true, true> : k_lora_expand<W, true, false>)
+                  : (vecy ? k_lora_expand<W, false, true> : k_lora_expand<W, false, false>);
+  return launch(fn, dim3((unsigned)ceil_div(p.N, p.span), tiles + copies), kExpandThreads, smem, 1, true, stream, p);
+}
+
+struct Carve {
+  size_t arrays, sort, v, total;
+};
+Carve carve(int M, int S, int R) {
+  Carve c;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = (size_t)round_up((int64_t)(off + bytes), 256);
+    return at;
+  };
+  c.arrays = take(4 * (size_t)(round_up(S + 1, 4) + 2 * round_up(M, 4)));
+  c.sort = take(segment_workspace_bytes(M, S, 1, false));
+  c.v = take((size_t)M * round_up(R, 32) * 4);
+  c.total = off;
+  return c;
+}
+
+}  // namespace
+
+size_t lora_workspace_bytes(int M, int S, int R) { return M <= kLoraDecodeTokens ? 0 : carve(M, S, R).total; }
+
+cudaError_t launch_lora(const sq_lora_bank& bank, const float* x, int M, const int32_t* ids, const int32_t* offsets,
+                        const int32_t* order, const float* base, int64_t ldb, float* y, int64_t ldy, void* workspace,
+                        int32_t* status, bool pdl, int sm_count, cudaStream_t stream) {
+  Params p = {};
+  p.A = bank.A;
+  p.B = bank.B;
+  p.scale = bank.scale;
+  p.rank = bank.rank;
+  p.S = bank.S;
+  p.R = bank.R;
+  p.K = bank.K;
+  p.N = bank.N;
+  p.x = x;
+  p.M = M;
+  p.ids = ids;
+  p.base = base;
+  p.ldb = ldb;
+  p.y = y;
+  p.ldy = ldy;
+  p.offsets = offsets;
+  p.order = order;
+  p.Rp = (int)round_up(bank.R, 32);
+  p.status = status;
+  p.pdl = pdl ? 1 : 0;
+  void* sort_ws = nullptr;
+  int32_t* arrays = nullptr;
+  if (M > kLoraDecodeTokens) {
+    const Carve c = carve(M, bank.S, bank.R);
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    arrays = reinterpret_cast<int32_t*>(w + c.arrays);
+    sort_ws = w + c.sort;
+    p.v = reinterpret_cast<float*>(w + c.v);
+  }
+  if (bank.type == SQ_TYPE_F16) return launch_type<__half>(p, sort_ws, arrays, sm_count, stream);
+  if (bank.type == SQ_TYPE_BF16) return launch_type<__nv_bfloat16>(p, sort_ws, arrays, sm_count, stream);
+  return launch_type<float>(p, sort_ws, arrays, sm_count, stream);
+}
+
+}  // namespace sq

@@ -581,6 +581,57 @@ sq_status sq_combine(const float *z, int32_t rows, const float *gates, const int
                      int32_t T, int32_t k, int32_t N, const float *base, float *out,
                      int32_t *dev_status, uint32_t flags, void *stream);
 
+/* Element types of an adapter bank. */
+#define SQ_TYPE_F32 0
+#define SQ_TYPE_F16 1
+#define SQ_TYPE_BF16 2
+
+/*
+ * Low-rank adapters beside a shared projection: S pairs A_a [rank_a][K],
+ * B_a [N][rank_a] in rows of one [S][R][K] and one [S][N][R] array.
+ *   type   SQ_TYPE_*: the element type of A and B
+ *   scale  [S] f32, device: the factor of each adapter
+ *   rank   [S] i32, device, each in [0, R] (clamped to it), or NULL: all R.  What
+ *          lies past an adapter's rank is not used, whatever it holds.
+ */
+typedef struct {
+  int32_t S, R, K, N; /* adapters, largest rank (<= 256), input channels (<= 65536), columns of y */
+  int32_t type;
+  const void *A;
+  const void *B;
+  const float *scale;
+  const int32_t *rank;
+} sq_lora_bank;
+
+/*
+ * The adapters' part of a projection's output, for tokens of many requests:
+ *   y[t][:] = base[t][:] + scale_a B_a (A_a x[t]),   a = ids[t]
+ * A token with id -1 has no adapter: y[t] = base[t].  Binary32 x, base, y;
+ * every product and sum is formed in binary32 or better.
+ *   x        [M][K] f32, 1 <= M <= 2^20
+ *   ids      [M] i32, device, in [-1, S), S <= 1024 (anything else counts as -1
+ *            and sets SQ_ERR_INVALID_ARG)
+ *   offsets, order   the sort of ids (sq_segment), where the caller keeps it for
+ *            several projections of one step; both NULL: sorted in this call.
+ *            Not used for M <= 64.
+ *   base     rows of N f32, ld_base floats apart; NULL: 0.  May be y itself (with
+ *            the same row stride); then the rows without an adapter are not
+ *            touched.  Otherwise base and y may not overlap.
+ *   y        rows of N f32, ld_y floats apart (a slice of a wider projection);
+ *            columns outside the slice are left as they were
+ *   workspace  sq_lora_workspace_bytes(bank, M) bytes (0 for M <= 64), 16-byte
+ *            aligned; scratch, no zeroing.  Calls that may overlap in time need
+ *            their own.
+ * base and y need 4-byte alignment only (16-byte rows are faster).  A token whose
+ * A_a x is not finite sets SQ_ERR_NONFINITE; its row of y is then not finite, the
+ * other rows are unaffected.  flags: SQ_LAUNCH_PDL.
+ */
+size_t sq_lora_workspace_bytes(const sq_lora_bank *bank, int32_t M);
+sq_status sq_lora_add(const sq_lora_bank *bank, const float *x, int32_t M, const int32_t *ids,
+                      const int32_t *offsets, const int32_t *order, const float *base,
+                      int64_t ld_base, float *y, int64_t ld_y, void *workspace, size_t ws_bytes,
+                      int32_t *dev_status, uint32_t flags, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -112,3 +112,30 @@ def test_grouped_linear_refusals(L):
                dict(n=(1 << 24) + 1)):
         assert call(**kw) == 2, kw
     assert call(flags=2) == 1
+
+
+def test_lora_refusals(L):
+    def bank(**kw):
+        b = sq.SqLoraBank(S=4, R=16, K=256, N=512, type=sq.SQ_TYPE_BF16, A=1 << 41, B=1 << 41, scale=1 << 41, rank=None)
+        for k, v in kw.items():
+            setattr(b, k, v)
+        return b
+
+    def call(b=None, x=P, M=32, ids=P, off=None, order=None, base=P, ldb=512, y=P, ldy=512, ws=None, wn=0, flags=0):
+        b = b or bank()
+        return L.sq_lora_add(ctypes.byref(b), x, M, ids, off, order, base, ldb, y, ldy, ws, wn, None, flags, None)
+    for kw in (dict(A=None), dict(B=None), dict(scale=None), dict(type=3)):
+        assert call(bank(**kw)) == 1, kw
+    for kw in (dict(S=0), dict(S=1025), dict(R=0), dict(R=257), dict(K=0), dict(K=65537), dict(N=0)):
+        assert call(bank(**kw)) == 2, kw
+    for kw in (dict(A=(1 << 41) + 8), dict(rank=(1 << 41) + 4)):
+        assert call(bank(**kw)) == 3, kw
+    for name in ("x", "ids", "y"):
+        assert call(**{name: None}) == 1, name
+    assert call(off=P) == 1 and call(order=P) == 1 and call(flags=2) == 1
+    assert call(M=0) == 2 and call(M=(1 << 20) + 1) == 2 and call(ldy=511) == 2 and call(ldb=511) == 2
+    assert call(ldb=1024, ldy=512) == 1  # in place (base is y) with another row stride
+    assert call(x=BAD) == 3 and call(ids=BAD) == 3 and call(y=ctypes.c_void_p((1 << 41) + 2), base=None) == 3
+    assert L.sq_lora_workspace_bytes(ctypes.byref(bank()), 64) == 0
+    need = L.sq_lora_workspace_bytes(ctypes.byref(bank()), 65)
+    assert need >= 65 * 32 * 4 and call(M=65) == 8 and call(M=65, ws=P, wn=need - 1) == 8
