@@ -40,6 +40,7 @@ SOURCES = [
     ("sq_probe.cu", []),
     ("sq_route.cu", []),
     ("sq_grouped.cu", []),
+    ("sq_grouped_tc5.cu", []),
     ("sq_lora.cu", []),
 ]
 

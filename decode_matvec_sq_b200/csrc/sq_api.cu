@@ -697,7 +697,9 @@ sq_status sq_expert_view(const sq_packed_weight* stack, int32_t E, int32_t N, in
 
 size_t sq_grouped_linear_workspace_bytes(const sq_packed_weight* stack, int32_t E, int32_t N, int32_t n) {
   if (check_stack(stack, E, N) != SQ_OK || n < 1 || n > kMaxEntries) return 0;
-  return grouped_workspace_bytes(E, N, stack->K, n);
+  DeviceInfo d;
+  if (!current_device(&d)) return 0;
+  return grouped_workspace_bytes(E, stack->K, n, stack->layout == SQ_LAYOUT_TILES_ASYM, d.sm_count);
 }
 
 sq_status sq_grouped_linear(const sq_packed_weight* stack, int32_t E, int32_t N, const int8_t* xq, const float* sx,
@@ -714,10 +716,10 @@ sq_status sq_grouped_linear(const sq_packed_weight* stack, int32_t E, int32_t N,
   if (!aligned16(xq) || !aligned16(sx) || !aligned16(offsets) || !aligned16(y) || (order && !aligned16(order)) ||
       (n_out > 0 && (!aligned16(idx) || !aligned16(x_out))) || (workspace && !aligned16(workspace)))
     return SQ_ERR_ALIGN;
-  const size_t need = grouped_workspace_bytes(E, N, stack->K, n);
-  if (need && (!workspace || ws_bytes < need)) return SQ_ERR_WORKSPACE;
   DeviceInfo d;
   if ((st = check_device(&d)) != SQ_OK) return st;
+  const size_t need = grouped_workspace_bytes(E, stack->K, n, stack->layout == SQ_LAYOUT_TILES_ASYM, d.sm_count);
+  if (need && (!workspace || ws_bytes < need)) return SQ_ERR_WORKSPACE;
   GroupedArgs a;
   a.res = stack->res_q;
   a.sign = stack->sign_bits;

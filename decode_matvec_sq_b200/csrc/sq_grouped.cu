@@ -429,9 +429,15 @@ cudaError_t launch_kind(const GroupedArgs& a, int sm_count, cudaStream_t stream)
 
 }  // namespace
 
-size_t grouped_workspace_bytes(int, int, int, int64_t) { return 0; }
+bool grouped_many(int E, int64_t n) { return n >= 16 * (int64_t)E; }
 
-cudaError_t launch_grouped(const GroupedArgs& a, void*, int sm_count, cudaStream_t stream) {
+size_t grouped_workspace_bytes(int E, int K, int64_t n, bool asym, int sm_count) {
+  return grouped_many(E, n) && !asym ? grouped_tc5_workspace_bytes(K, n, sm_count) : 0;
+}
+
+cudaError_t launch_grouped(const GroupedArgs& a, void* workspace, int sm_count, cudaStream_t stream) {
+  if (grouped_many(a.E, a.n) && grouped_tc5_supported(a.n_out, a.zero != nullptr))
+    return launch_grouped_tc5(a, workspace, sm_count, stream);
   if (a.n <= 8) return launch_kind<1>(a, sm_count, stream);
   return launch_kind<2>(a, sm_count, stream);
 }

@@ -134,7 +134,11 @@ cudaError_t launch_combine(const float* z, int rows, const float* gates, const i
 
 // The expert-grouped linear layer (sq_grouped.cuh holds the arguments).
 struct GroupedArgs;
-size_t grouped_workspace_bytes(int E, int N, int K, int64_t n);
+bool grouped_many(int E, int64_t n);  // enough places for the tcgen05 kernel
+size_t grouped_workspace_bytes(int E, int K, int64_t n, bool asym, int sm_count);
+bool grouped_tc5_supported(int n_out, bool asym);
+size_t grouped_tc5_workspace_bytes(int K, int64_t n, int sm_count);
+cudaError_t launch_grouped_tc5(const GroupedArgs& a, void* workspace, int sm_count, cudaStream_t stream);
 cudaError_t launch_grouped(const GroupedArgs& a, void* workspace, int sm_count, cudaStream_t stream);
 
 // Low-rank adapters (sq_lora.cu).  Up to kLoraDecodeTokens tokens take one
