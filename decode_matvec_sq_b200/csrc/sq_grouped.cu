@@ -429,7 +429,7 @@ cudaError_t launch_kind(const GroupedArgs& a, int sm_count, cudaStream_t stream)
 
 }  // namespace
 
-bool grouped_many(int E, int64_t n) { return n >= 16 * (int64_t)E; }
+bool grouped_many(int E, int64_t n) { return n >= 24 * (int64_t)E; }
 
 size_t grouped_workspace_bytes(int E, int K, int64_t n, bool asym, int sm_count) {
   return grouped_many(E, n) && !asym ? grouped_tc5_workspace_bytes(K, n, sm_count) : 0;

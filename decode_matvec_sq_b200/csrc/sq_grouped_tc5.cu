@@ -6,25 +6,25 @@
 //   y = sx (alpha T + sum_g s_g R_g) + sum_i What[r][idx_i] x_out[i].
 //
 // A tile is 128 weight rows of one expert (MMA M, one tensor-memory lane each)
-// x up to 256 of its tokens (MMA N, a multiple of 32), so that a row's scales are
+// x up to 160 of its tokens (MMA N, a multiple of 32), so that a row's scales are
 // one thread's scalars.  Persistent CTAs, one per SM, walk over the tiles of all
 // experts, token tiles fastest (they share the weights in L2).
-//   warp 0: bulk copies of a channel group's eight packed row blocks (2 KB codes,
-//     256 B signs, 64 B scales each) into the raw ring;
+//   warp 0: tensor copies of a channel group's eight packed row blocks (codes, bits)
+//     into the raw ring;
 //   warp 2: TMA of the group's activation codes (rows in place order);
-//   warps 4-11: (a) turn the raw row blocks into the two K-major, 128-byte-
-//     swizzled int8 operands, codes and +-1 (0 outside the mask) trunk bytes;
-//     (b) read each group's R from tensor memory and add s_g R to binary32
-//     registers; (c) at the end of a tile read T, add the outlier channels and
-//     write y.  Warps 4-7 hold the first half of the tile's tokens, 8-11 the
-//     second;
-//   warp 1 (one lane): per group, R of the first half, R of the second half
-//     (each free again while the other MMAs run), then T over all tokens.
-// What bounds it: shared-memory bandwidth.  Per group the copies write 19 + 32 KB,
-// the operand warps read 16 and write 32 KB, the MMAs read the operands of R twice
-// (one for each half) and of T once, 112 KB at 256 tokens; 128 bytes a clock
-// give 1750 clocks for 128 x 256 x 128, twice that of the MMAs alone.  Hence
-// the wide tile: 128 tokens would cost 1170.
+//   warps 4-11: turn the raw row blocks into the two K-major, 128-byte-swizzled
+//     int8 operands, codes and +-1 (0 outside the mask) trunk bytes;
+//   warp 3: the dequantized weights of the group's outlier channels;
+//   warp 1: per group, R into one of two tensor-memory buffers, and T;
+//   warps 12-19: read each group's R and add s_g R to binary32 registers; at the
+//     end of a tile read T, add the outlier channels and write y (warps 12-15 the
+//     first half of the tile's tokens, 16-19 the second).
+// What bounds it: the hand-overs.  With every copy, operand and promotion taken out
+// a group still costs 1400 clocks of barrier round trips in a chain of five roles
+// (16 MMAs a group on five barriers cost 2300; the eight here on two 1800 at 160
+// tokens, of which shared-memory traffic alone would be 1400).  Hence the wide
+// tile, one barrier per stage for both operands, and group scales that the
+// promotion reads from memory itself.
 // The sums are integers because the tensor cores' binary32 sums are not exact
 // enough: 16-bit operands accumulated over K = 4096 measured 4.4e-6 relative
 // error (a truncation that grows with K; 1.6e-5 at 14336), the integer sums none.
@@ -43,56 +43,66 @@ namespace {
 using tc05::fence_after;
 using tc05::fence_before;
 
-constexpr int kThreads = 384;
-constexpr int kComputeThreads = 256;
-constexpr int kLaunchRegs = 168;    // registers a thread at launch, as 384 threads allow
-constexpr int kProducerRegs = 40, kComputeRegs = 232;
+constexpr int kThreads = 640;
+constexpr int kLaunchRegs = 96;     // registers a thread at launch, as 640 threads allow
+constexpr int kProducerRegs = 64, kOperandRegs = 64, kPromoteRegs = 144;
+constexpr int kOperandWarps = 8;    // one row block each
+constexpr int kSets = 2;            // warpgroups of the promotion, half of the tokens each
+constexpr int kPromoteThreads = 128 * kSets;
 constexpr int kRows = 128;          // weight rows per tile (MMA M)
-constexpr int kTokens = 256;        // most tokens per tile (MMA N)
+constexpr int kTokens = 160;        // most tokens per tile (MMA N)
+constexpr int kTokenUnit = 16 * kSets;  // MMA N is a multiple of this
+constexpr int kCols = kTokens / kSets, kPieces = kCols / 16;
 constexpr int kBlocks = kRows / kTileRows;
-constexpr uint32_t kTmemCols = 512; // T [0, 256), R of half h from 256 + 128 h
-constexpr int kMaxBufs = 4;         // R buffers per half (128 columns; small tiles hold several)
-constexpr int kRawStages = 2, kAStages = 3, kBStages = 2;
+constexpr uint32_t kTmemCols = 512; // T [0, 160), R of group g at 160 + 160 (g % 2)
+constexpr int kRawStages = 4, kStages = 2;
 constexpr int kABytes = kRows * kTileK;      // one operand: 16 KB
-constexpr int kBBytes = kTokens * kTileK;    // 32 KB
-constexpr int kScaleSlots = 4;
+constexpr int kBBytes = kTokens * kTileK;    // 20 KB
+constexpr int kStageBytes = 2 * kABytes + kBBytes;
+static_assert(kStageBytes % 1024 == 0 && kCols % 16 == 0 && 3 * kTokens <= (int)kTmemCols, "tile layout");
 constexpr int kMaxOut = 128;        // outlier channels this kernel takes
+constexpr int kOutPass = 8;         // of them in shared memory at a time
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 template <bool MASK>
 struct Raw {
   static constexpr int kSign = kBlocks * 2048;
   static constexpr int kMask = kSign + kBlocks * 256;
-  static constexpr int kScale = MASK ? kMask + kBlocks * 256 : kMask;
-  static constexpr int kBytes = kScale + kBlocks * 64;
+  static constexpr int kBytes = MASK ? kMask + kBlocks * 256 : kMask;
 };
 
 struct Aux {
   uint64_t raw_full[kRawStages], raw_empty[kRawStages];
-  uint64_t a_full[kAStages], a_empty[kAStages];
-  uint64_t b_full[kBStages], b_empty[kBStages];
-  uint64_t accf[2][kMaxBufs], acce[2][kMaxBufs];
-  uint64_t t_full, t_empty, wo_full, wo_empty, drain;
+  uint64_t full[kStages], empty[kStages];
+  uint64_t accf[2], acce[2];
+  uint64_t t_full, t_empty, wo_full, out, drain;
   uint32_t tmem_base;
   int abort;
   int part[kThreads / 32];
-  float scale[kScaleSlots][kRows];
+};
+
+// The stack's arrays as rows of row blocks, so that one tensor copy brings eight row
+// blocks' tiles of a channel group (a bulk copy for each of the 24 pieces cost 90
+// clocks of the issuing warp, 2200 a group).
+struct WeightMaps {
+  CUtensorMap codes, sign, mask;
 };
 
 struct Params {
   GroupedArgs a;
   const float* sxp;   // [n] token scales in place order
-  const float* xop;   // [n][n8] outlier activations in place order
-  int n8;             // n_out rounded up to 4
-  float* wout;        // [CTAs][kMaxOut][kRows] outlier weights of the CTA's tile
+  const float* xop;   // [n_out][n] outlier activations in place order
+  float* wout;        // [CTAs][2][kMaxOut][kRows] outlier weights of the CTA's tiles
   int rt;             // row tiles per expert
-  int off_b, off_raw, off_aux, off_pre, off_ostart;  // shared-memory offsets
+  int off_raw, off_xo, off_aux, off_pre, off_ostart;  // shared-memory offsets
 };
 
-// D (s32) (+)= A (s8) B (s8), both K-major; M = 128, N = n.
-__device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, int n, bool acc) {
-  const uint32_t idesc =
-      (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+// D (s32) (+)= A (s8) B (s8), both K-major; M = 128, N = n.  A K step of 32 bytes is
+// 2 in a descriptor's address field.
+__device__ __forceinline__ uint32_t idesc_of(int n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+__device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
@@ -101,10 +111,29 @@ __device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, int n
 }
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Aux* aux, const Params& p) {
-  if (mbar_wait(bar, parity, kWaitNs)) return true;
+  // (the clock is read once in 32 tries: reading it at every one slows the SM)
+  uint64_t t0 = 0;
+  for (uint32_t n = 0;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 31u) == 31u) {
+      const uint64_t now = global_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitNs) break;
+    }
+  }
   set_status(p.a.status, SQ_ERR_TIMEOUT);
   atomicExch(&aux->abort, 1);
   return false;
+}
+// The same for a whole warp, with a warp-uniform result (so that what follows may
+// run on the uniform datapath).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Aux* aux, const Params& p) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, aux, p));
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(pred));
+  return pred != 0;
 }
 __device__ __forceinline__ bool aborted(const Aux* aux) {
   return *reinterpret_cast<const volatile int*>(&aux->abort) != 0;
@@ -123,27 +152,69 @@ __device__ __forceinline__ uint32_t trunk_word(uint32_t sign, uint32_t mask, int
 __device__ __forceinline__ uint32_t swap_halves(uint32_t b) {
   return ((b >> 4) & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
 }
-// 16 consecutive TMEM columns of this thread's lane.
+// 16 consecutive TMEM columns of this thread's lane: the load, and the wait after
+// which r may be used.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, int (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-// |r| < 2^22
-__device__ __forceinline__ float small_int_to_float(int r) {
-  return __fsub_rn(__int_as_float(r + 0x4B400000), 12582912.0f);
+__device__ __forceinline__ void tmem_wait16(int (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
 }
-
+// f(c, r) for the 16-column pieces c of [0, h) (h <= kCols) from column `src`, two
+// pieces' loads in flight per wait (columns past h are read, not used).
+template <class F>
+__device__ __forceinline__ void tmem_pieces(uint32_t src, int h, F f) {
+#pragma unroll
+  for (int c = 0; c < kPieces; c += 2) {
+    if (16 * c < h) {
+      int r[2][16];
+      tmem_ld16(src + 16 * c, r[0]);
+      if (c + 1 < kPieces) tmem_ld16(src + 16 * (c + 1), r[1]);
+      tmem_wait16(r[0]);
+      if (c + 1 < kPieces) tmem_wait16(r[1]);
+      f(c, r[0]);
+      if (c + 1 < kPieces && 16 * (c + 1) < h) f(c + 1, r[1]);
+    }
+  }
+}
+// Two binary32 values in a 64-bit register (first in the low half) and the packed
+// operations on them: half the instructions of the promotion.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
 // One tile: an expert's 128 rows x up to 256 of its places.
 struct Tile {
   int rb0;       // first row block in the stack
   int blocks;    // row blocks of the expert in this tile (1..8)
   int row0;      // first row in the expert
   int p0, cnt;   // first place, tokens
-  int n;         // MMA N: cnt rounded up to 32
+  int n;         // MMA N: cnt rounded up to kTokenUnit
 };
 __device__ __forceinline__ Tile tile_at(const Params& p, const int* pre, int item) {
   const GroupedArgs& a = p.a;
@@ -152,22 +223,19 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const int* pre, int ite
   const int tt = local % ntt, rt = local / ntt;
   const int2 seg = segment_bounds(a.offsets, a.n, e, nullptr);
   const int total = seg.y - seg.x;
-  const int ts = ((total + ntt - 1) / ntt + 31) & ~31;  // <= 256, and (ntt - 1) ts < total
+  const int ts = ((total + ntt - 1) / ntt + kTokenUnit - 1) / kTokenUnit * kTokenUnit;  // (ntt - 1) ts < total
   Tile t;
   t.rb0 = e * a.rbe + rt * kBlocks;
   t.blocks = min(kBlocks, a.rbe - rt * kBlocks);
   t.row0 = rt * kRows;
   t.p0 = seg.x + tt * ts;
   t.cnt = min(ts, total - tt * ts);
-  t.n = (t.cnt + 31) & ~31;
+  t.n = (t.cnt + kTokenUnit - 1) / kTokenUnit * kTokenUnit;
   return t;
 }
-// R buffers per half of a tile with MMA N = n: 128 columns hold that many n/2.
-__device__ __forceinline__ int r_bufs(int n) { return n > 128 ? 1 : n > 64 ? 2 : kMaxBufs; }
-
 template <bool MASK>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_grouped_tc5(const __grid_constant__ CUtensorMap tmB, const Params p) {
+    k_grouped_tc5(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ WeightMaps wm, const Params p) {
   using RW = Raw<MASK>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -175,30 +243,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* pre = reinterpret_cast<int*>(smem + p.off_pre);
   int* ostart = reinterpret_cast<int*>(smem + p.off_ostart);
   const GroupedArgs& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kRawStages; ++s) {
       mbar_init(&aux->raw_full[s], 1);
-      mbar_init(&aux->raw_empty[s], kComputeThreads / 32);
+      mbar_init(&aux->raw_empty[s], kOperandWarps + 1);
     }
-    for (int s = 0; s < kAStages; ++s) {
-      mbar_init(&aux->a_full[s], kComputeThreads / 32);
-      mbar_init(&aux->a_empty[s], 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&aux->full[s], kOperandWarps + 1);
+      mbar_init(&aux->empty[s], 1);
     }
-    for (int s = 0; s < kBStages; ++s) {
-      mbar_init(&aux->b_full[s], 1);
-      mbar_init(&aux->b_empty[s], 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&aux->accf[b], 1);
+      mbar_init(&aux->acce[b], kPromoteThreads / 32);
     }
-    for (int h = 0; h < 2; ++h)
-      for (int b = 0; b < kMaxBufs; ++b) {
-        mbar_init(&aux->accf[h][b], 1);
-        mbar_init(&aux->acce[h][b], 4);
-      }
     mbar_init(&aux->t_full, 1);
-    mbar_init(&aux->t_empty, kComputeThreads / 32);
-    mbar_init(&aux->wo_full, kComputeThreads / 32);
-    mbar_init(&aux->wo_empty, kComputeThreads / 32);
+    mbar_init(&aux->t_empty, kPromoteThreads / 32);
+    mbar_init(&aux->wo_full, 1);
+    mbar_init(&aux->out, kPromoteThreads / 32);
     mbar_init(&aux->drain, 1);
     aux->abort = 0;
     fence_barrier_init();
@@ -238,24 +301,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
         const Tile t = tile_at(p, pre, item);
-        // lane: row block lane % 8 of the array lane / 8 (blocks past the
-        // expert repeat its last; their rows are not written)
-        const int64_t rb = t.rb0 + min(lane & 7, t.blocks - 1);
         for (int kb = 0; kb < a.tpr; ++kb, ++g) {
           const int s = (int)(g % kRawStages);
           const uint32_t use = g / kRawStages;
-          if (g >= kRawStages) ok = wait_or_abort(&aux->raw_empty[s], (use & 1u) ^ 1u, aux, p);
+          if (g >= kRawStages) ok = warp_wait(&aux->raw_empty[s], (use & 1u) ^ 1u, aux, p);
           ok = __all_sync(0xffffffffu, ok && !aborted(aux));
           if (!ok) break;
           uint8_t* st = smem + p.off_raw + s * RW::kBytes;
-          if (lane == 0) mbar_arrive_expect_tx(&aux->raw_full[s], RW::kBytes);
+          // (row blocks past the expert are the next expert's, past the stack zero;
+          // their rows are not written)
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&aux->raw_full[s], RW::kBytes);
+            tc05::tma_load_2d(st, &wm.codes, kb * 256, t.rb0, &aux->raw_full[s]);
+            tc05::tma_load_2d(st + RW::kSign, &wm.sign, kb * 32, t.rb0, &aux->raw_full[s]);
+            if (MASK) tc05::tma_load_2d(st + RW::kMask, &wm.mask, kb * 32, t.rb0, &aux->raw_full[s]);
+          }
           __syncwarp();
-          const int64_t tile = rb * a.tpr + kb;
-          const int b = lane & 7;
-          if (lane < 8) tc05::bulk_load(st + b * 2048, a.res + tile * 2048, 2048, &aux->raw_full[s]);
-          else if (lane < 16) tc05::bulk_load(st + RW::kSign + b * 256, a.sign + tile * 64, 256, &aux->raw_full[s]);
-          else if (lane < 24) tc05::bulk_load(st + RW::kScale + b * 64, a.scale + tile * 16, 64, &aux->raw_full[s]);
-          else if (MASK) tc05::bulk_load(st + RW::kMask + b * 256, a.mask + tile * 64, 256, &aux->raw_full[s]);
           last[s] = (int)use;
         }
       }
@@ -264,266 +325,299 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < kRawStages; ++s)
           if (last[s] >= 0) (void)mbar_wait(&aux->raw_full[s], (uint32_t)last[s] & 1u, kWaitNs);
       }
-    } else if (warp == 2 && lane == 0) {
+    } else if (warp == 2) {
       // ---- activation producer: n rows of 128 codes per channel group
       uint32_t g = 0;
-      int last[kBStages];
+      int last[kStages];
 #pragma unroll
-      for (int s = 0; s < kBStages; ++s) last[s] = -1;
+      for (int s = 0; s < kStages; ++s) last[s] = -1;
       bool ok = true;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
         const Tile t = tile_at(p, pre, item);
         for (int kb = 0; kb < a.tpr; ++kb, ++g) {
-          const int s = (int)(g % kBStages);
-          const uint32_t use = g / kBStages;
-          if (g >= kBStages) ok = wait_or_abort(&aux->b_empty[s], (use & 1u) ^ 1u, aux, p);
-          ok = ok && !aborted(aux);
+          const int s = (int)(g % kStages);
+          const uint32_t use = g / kStages;
+          if (g >= kStages) ok = warp_wait(&aux->empty[s], (use & 1u) ^ 1u, aux, p);
+          ok = __all_sync(0xffffffffu, ok && !aborted(aux));
           if (!ok) break;
-          uint8_t* st = smem + p.off_b + s * kBBytes;
-          mbar_arrive_expect_tx(&aux->b_full[s], (uint32_t)t.n * kTileK);
-          for (int r = 0; r < t.n; r += 32)
-            tc05::tma_load_2d(st + r * kTileK, &tmB, kb * kTileK, t.p0 + r, &aux->b_full[s]);
+          uint8_t* st = smem + s * kStageBytes + 2 * kABytes;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&aux->full[s], (uint32_t)t.n * kTileK);
+            for (int r = 0; r < t.n; r += kTokenUnit)
+              tc05::tma_load_2d(st + r * kTileK, &tmB, kb * kTileK, t.p0 + r, &aux->full[s]);
+          }
+          __syncwarp();
           last[s] = (int)use;
         }
       }
+      // winding down: every requested stage must have landed.  The stage's barrier
+      // also counts the operand warps, which may have stopped: they arrive once
+      // more for it when they leave
       if (aborted(aux)) {
 #pragma unroll
-        for (int s = 0; s < kBStages; ++s)
-          if (last[s] >= 0) (void)mbar_wait(&aux->b_full[s], (uint32_t)last[s] & 1u, kWaitNs);
+        for (int s = 0; s < kStages; ++s)
+          if (last[s] >= 0) (void)mbar_wait(&aux->full[s], (uint32_t)last[s] & 1u, kWaitNs);
       }
-    } else if (warp == 1 && lane == 0) {
-      // ---- MMA issuer
+    } else if (warp == 3) {
+      // ---- outlier channels: their dequantized weights for the tile's 128 rows
       uint32_t g = 0, n_items = 0;
-      uint32_t used[2] = {0u, 0u}, phase[2] = {0u, 0u};  // per half: buffers ever used, their acce parity
       bool ok = true;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++n_items) {
         const Tile t = tile_at(p, pre, item);
-        const int h = t.n / 2, bufs = r_bufs(t.n);
+        float* wout = p.wout + ((int64_t)blockIdx.x * 2 + (n_items & 1u)) * kMaxOut * kRows + lane;
         for (int kb = 0; kb < a.tpr; ++kb, ++g) {
-          const int sa = (int)(g % kAStages), sb = (int)(g % kBStages), b = kb % bufs;
-          ok = wait_or_abort(&aux->a_full[sa], (g / kAStages) & 1u, aux, p) &&
-               wait_or_abort(&aux->b_full[sb], (g / kBStages) & 1u, aux, p);
-          // (R buffers lie differently in the next tile: all of this one's are free)
-          if (ok && kb == 0 && n_items > 0) ok = wait_or_abort(&aux->t_empty, (n_items & 1u) ^ 1u, aux, p);
+          const int s = (int)(g % kRawStages);
+          ok = warp_wait(&aux->raw_full[s], (g / kRawStages) & 1u, aux, p) && !aborted(aux);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint8_t* st = smem + p.off_raw + s * RW::kBytes;
+          for (int o = ostart[kb]; o < ostart[kb + 1]; ++o) {
+            const int j = __ldg(a.idx + o) & 127, w = (j & 31) >> 2, bit = tiled_bit_of(j & 31);
+            const int own = (lane & 7) * 4 + (j >> 5), R = (lane >> 3) & 1;  // rows lane % 16 of a block
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int blk = 2 * i + (lane >> 4);
+              const int64_t rb = t.rb0 + min(blk, t.blocks - 1);
+              const float al = __ldg(a.alpha + rb * kTileRows + (lane & 15));
+              const float sc = __ldg(a.scale + (rb * a.tpr + kb) * kTileRows + (lane & 15));
+              const int code = reinterpret_cast<const int8_t*>(
+                  st)[blk * 2048 + own * 64 + (w >> 1) * 16 + ((w & 1) * 2 + R) * 4 + (j & 3)];
+              const uint32_t sb = *reinterpret_cast<const uint32_t*>(st + RW::kSign + blk * 256 + own * 8 + 4 * R);
+              float tr = ((sb >> bit) & 1u) ? al : -al;
+              if constexpr (MASK) {
+                const uint32_t mb = *reinterpret_cast<const uint32_t*>(st + RW::kMask + blk * 256 + own * 8 + 4 * R);
+                if (!((mb >> bit) & 1u)) tr = 0.0f;
+              }
+              wout[o * kRows + 32 * i] = fmaf(sc, (float)code, tr);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&aux->raw_empty[s]);
+            if (kb == a.tpr - 1) mbar_arrive(&aux->wo_full);
+          }
+        }
+      }
+    } else if (warp == 1) {
+      // ---- MMA issuer (the whole warp walks; one lane issues)
+      uint32_t g = 0, n_items = 0;
+      bool ok = true;
+      const uint32_t s0 = smem_u32(smem);
+      for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++n_items) {
+        const Tile t = tile_at(p, pre, item);
+        const uint32_t idesc = idesc_of(t.n);
+        for (int kb = 0; kb < a.tpr; ++kb, ++g) {
+          const int s = (int)(g % kStages), b = (int)(g & 1u);
+          ok = warp_wait(&aux->full[s], (g / kStages) & 1u, aux, p) &&
+               (g < 2 || warp_wait(&aux->acce[b], ((g >> 1) & 1u) ^ 1u, aux, p));
           if (!ok) break;
           fence_after();
-          const uint32_t ca = smem_u32(smem + sa * 2 * kABytes), ta = ca + kABytes;
-          const uint32_t xb = smem_u32(smem + p.off_b + sb * kBBytes);
+          const uint64_t da = tc05::sw128_desc(s0 + s * kStageBytes);
+          const uint64_t dt = da + (kABytes >> 4), db = da + (2 * kABytes >> 4);
+          const uint32_t d = tmem + kTokens + kTokens * b;
+          if (elect_one()) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if ((used[half] >> b) & 1u) {
-              ok = wait_or_abort(&aux->acce[half][b], (phase[half] >> b) & 1u, aux, p);
-              if (!ok) break;
-              phase[half] ^= 1u << b;
-              fence_after();
-            }
-            used[half] |= 1u << b;
-            const uint32_t d = tmem + kTokens + 128 * half + b * h;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_i8(d, tc05::sw128_desc(ca + 32 * kk), tc05::sw128_desc(xb + half * h * kTileK + 32 * kk), h, kk > 0);
-            tc05::mma_commit(&aux->accf[half][b]);
+            for (int kk = 0; kk < 4; ++kk) mma_i8(d, da + 2 * kk, db + 2 * kk, idesc, kk > 0);
+            tc05::mma_commit(&aux->accf[b]);
           }
-          if (!ok) break;
+          __syncwarp();
+          if (kb == 0 && n_items > 0) {  // T of the tile before has been read
+            ok = warp_wait(&aux->t_empty, (n_items & 1u) ^ 1u, aux, p);
+            if (!ok) break;
+            fence_after();
+          }
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_i8(tmem, tc05::sw128_desc(ta + 32 * kk), tc05::sw128_desc(xb + 32 * kk), t.n, kb > 0 || kk > 0);
-          tc05::mma_commit(&aux->a_empty[sa]);
-          tc05::mma_commit(&aux->b_empty[sb]);
+            for (int kk = 0; kk < 4; ++kk) mma_i8(tmem, dt + 2 * kk, db + 2 * kk, idesc, kb > 0 || kk > 0);
+            tc05::mma_commit(&aux->empty[s]);
+            if (kb == a.tpr - 1) tc05::mma_commit(&aux->t_full);
+          }
+          __syncwarp();
         }
-        if (ok) tc05::mma_commit(&aux->t_full);
       }
       if (aborted(aux)) {  // the MMAs issued must be done before the tensor memory is freed
-        tc05::mma_commit(&aux->drain);
+        if (elect_one()) tc05::mma_commit(&aux->drain);
+        __syncwarp();
         (void)mbar_wait(&aux->drain, 0u, kWaitNs);
       }
     }
-  } else {
-    // ---- operands, promotion, epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
-    const int cw = warp - 4;                 // row block that this warp turns into operands
-    const int half = cw >> 2, q = warp & 3;  // tokens; tensor-memory lane quarter
-    const int gid = lane >> 2, tid4 = lane & 3;
-    const bool hi = tid4 >= 2;               // takes its two 8-channel pairs in the other order
-    const int my_row = 32 * q + lane;
-    float* wout = p.wout + (int64_t)blockIdx.x * kMaxOut * kRows;
-    uint32_t gc = 0, gp = 0, n_items = 0;    // groups converted, promoted; tiles finished
-    uint32_t accp = 0;                       // parity of accf[half][b]
-    int citem = blockIdx.x, ckb = 0;         // the conversion runs one group ahead, across tiles
+  } else if (warp < 4 + kOperandWarps) {
+    // ---- operands: one row block of each group per warp
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOperandRegs));
+    const int cw = warp - 4, gid = lane >> 2, tid4 = lane & 3;
+    const bool hi = tid4 >= 2;  // takes its two 16-channel pieces in the other order
+    uint32_t g = 0;
     bool ok = true;
-
-    // this warp's row block of the next group into operand stage gc % kAStages
-    auto convert = [&]() {
-      if (citem >= items || !ok) return;
-      const int sr = (int)(gc % kRawStages), sa = (int)(gc % kAStages);
-      ok = wait_or_abort(&aux->raw_full[sr], (gc / kRawStages) & 1u, aux, p);
-      if (ok && gc >= kAStages) ok = wait_or_abort(&aux->a_empty[sa], ((gc / kAStages) & 1u) ^ 1u, aux, p);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      const uint8_t* st = smem + p.off_raw + sr * RW::kBytes;
-      const uint8_t* cb = st + cw * 2048 + lane * 64;
-      uint2 sg = *reinterpret_cast<const uint2*>(st + RW::kSign + cw * 256 + lane * 8);
-      uint2 mk = make_uint2(0u, 0u);
-      if constexpr (MASK) mk = *reinterpret_cast<const uint2*>(st + RW::kMask + cw * 256 + lane * 8);
-      if (hi) {
-        sg.x = swap_halves(sg.x);
-        sg.y = swap_halves(sg.y);
-        if constexpr (MASK) {
-          mk.x = swap_halves(mk.x);
-          mk.y = swap_halves(mk.y);
-        }
-      }
-      // row gid (and gid + 8) of the block: 128 bytes in a 1024-byte atom of 8
-      // rows, 16-byte chunk c at c ^ gid; channels 32 tid4 + 16 c' are chunk 2 tid4 + c'
-      uint8_t* ao = smem + sa * 2 * kABytes + cw * 2048 + gid * 128;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = hi ? i ^ 1 : i;  // 16 channels: words 4c .. 4c + 3
-        const uint4 u = *reinterpret_cast<const uint4*>(cb + 32 * c), v = *reinterpret_cast<const uint4*>(cb + 32 * c + 16);
-        uint8_t* o = ao + (((2 * tid4 + c) ^ gid) << 4);
-        *reinterpret_cast<uint4*>(o) = make_uint4(u.x, u.z, v.x, v.z);
-        *reinterpret_cast<uint4*>(o + 1024) = make_uint4(u.y, u.w, v.y, v.w);
-        // (the sign words are swapped alike, so the shifts are fixed)
-        *reinterpret_cast<uint4*>(o + kABytes) =
-            make_uint4(trunk_word<MASK>(sg.x, mk.x, 4 * i), trunk_word<MASK>(sg.x, mk.x, 4 * i + 1),
-                       trunk_word<MASK>(sg.x, mk.x, 4 * i + 2), trunk_word<MASK>(sg.x, mk.x, 4 * i + 3));
-        *reinterpret_cast<uint4*>(o + kABytes + 1024) =
-            make_uint4(trunk_word<MASK>(sg.y, mk.y, 4 * i), trunk_word<MASK>(sg.y, mk.y, 4 * i + 1),
-                       trunk_word<MASK>(sg.y, mk.y, 4 * i + 2), trunk_word<MASK>(sg.y, mk.y, 4 * i + 3));
-      }
-      const float* sc = reinterpret_cast<const float*>(st + RW::kScale + cw * 64);
-      if (lane < 16) aux->scale[gc % kScaleSlots][16 * cw + lane] = sc[lane];
-      // outlier channels of this group: the dequantized weight of row `lane`
-      const int o0 = ostart[ckb], o1 = ostart[ckb + 1];
-      if (o0 < o1 && lane < 16) {
-        const Tile t = tile_at(p, pre, citem);
-        const float al = __ldg(a.alpha + (int64_t)(t.rb0 + min(cw, t.blocks - 1)) * kTileRows + lane);
-        for (int o = o0; o < o1; ++o) {
-          const int j = __ldg(a.idx + o) & 127, w = (j & 31) >> 2;
-          const int own = (lane & 7) * 4 + (j >> 5), R = lane >> 3, bit = tiled_bit_of(j & 31);
-          const int code = reinterpret_cast<const int8_t*>(st)[cw * 2048 + own * 64 + (w >> 1) * 16 +
-                                                               ((w & 1) * 2 + R) * 4 + (j & 3)];
-          const uint32_t sb = *reinterpret_cast<const uint32_t*>(st + RW::kSign + cw * 256 + own * 8 + 4 * R);
-          float tr = ((sb >> bit) & 1u) ? al : -al;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      for (int kb = 0; kb < a.tpr; ++kb, ++g) {
+        const int sr = (int)(g % kRawStages), sa = (int)(g % kStages);
+        ok = warp_wait(&aux->raw_full[sr], (g / kRawStages) & 1u, aux, p);
+        if (ok && g >= kStages) ok = warp_wait(&aux->empty[sa], ((g / kStages) & 1u) ^ 1u, aux, p);
+        ok = __all_sync(0xffffffffu, ok && !aborted(aux));
+        if (!ok) break;
+        const uint8_t* st = smem + p.off_raw + sr * RW::kBytes;
+        const uint8_t* cb = st + cw * 2048 + lane * 64;
+        uint2 sg = *reinterpret_cast<const uint2*>(st + RW::kSign + cw * 256 + lane * 8);
+        uint2 mk = make_uint2(0u, 0u);
+        if constexpr (MASK) mk = *reinterpret_cast<const uint2*>(st + RW::kMask + cw * 256 + lane * 8);
+        if (hi) {
+          sg.x = swap_halves(sg.x);
+          sg.y = swap_halves(sg.y);
           if constexpr (MASK) {
-            const uint32_t mb = *reinterpret_cast<const uint32_t*>(st + RW::kMask + cw * 256 + own * 8 + 4 * R);
-            if (!((mb >> bit) & 1u)) tr = 0.0f;
+            mk.x = swap_halves(mk.x);
+            mk.y = swap_halves(mk.y);
           }
-          wout[o * kRows + 16 * cw + lane] = fmaf(sc[lane], (float)code, tr);
+        }
+        // row gid (and gid + 8) of the block: 128 bytes in a 1024-byte atom of 8
+        // rows, 16-byte chunk c at c ^ gid; channels 32 tid4 + 16 c' are chunk 2 tid4 + c'
+        uint8_t* ao = smem + sa * kStageBytes + cw * 2048 + gid * 128;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c = hi ? i ^ 1 : i;  // 16 channels: words 4c .. 4c + 3
+          const uint4 u = *reinterpret_cast<const uint4*>(cb + 32 * c);
+          const uint4 v = *reinterpret_cast<const uint4*>(cb + 32 * c + 16);
+          uint8_t* o = ao + (((2 * tid4 + c) ^ gid) << 4);
+          *reinterpret_cast<uint4*>(o) = make_uint4(u.x, u.z, v.x, v.z);
+          *reinterpret_cast<uint4*>(o + 1024) = make_uint4(u.y, u.w, v.y, v.w);
+          // (the sign words are swapped alike, so the shifts are fixed)
+          *reinterpret_cast<uint4*>(o + kABytes) =
+              make_uint4(trunk_word<MASK>(sg.x, mk.x, 4 * i), trunk_word<MASK>(sg.x, mk.x, 4 * i + 1),
+                         trunk_word<MASK>(sg.x, mk.x, 4 * i + 2), trunk_word<MASK>(sg.x, mk.x, 4 * i + 3));
+          *reinterpret_cast<uint4*>(o + kABytes + 1024) =
+              make_uint4(trunk_word<MASK>(sg.y, mk.y, 4 * i), trunk_word<MASK>(sg.y, mk.y, 4 * i + 1),
+                         trunk_word<MASK>(sg.y, mk.y, 4 * i + 2), trunk_word<MASK>(sg.y, mk.y, 4 * i + 3));
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&aux->full[sa]);
+          mbar_arrive(&aux->raw_empty[sr]);
         }
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    // winding down after a timeout: the activation producer waits for the copies of
+    // the stages it has requested, on barriers that count these warps too
+    if (aborted(aux) && lane == 0)
+      for (int s = 0; s < kStages; ++s) mbar_arrive(&aux->full[s]);
+  } else {
+    // ---- promotion and epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPromoteRegs));
+    const int set = (warp - 4 - kOperandWarps) >> 2, q = warp & 3;  // half of the tokens; tensor-memory lane quarter
+    const int my_row = 32 * q + lane;
+    uint32_t g = 0, n_items = 0, n_sync = 0;
+    float* xo = reinterpret_cast<float*>(smem + p.off_xo);
+    bool ok = true;
+    // a barrier of these warps, with a bounded wait
+    auto out_sync = [&]() -> bool {
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&aux->raw_empty[sr]);
-        mbar_arrive(&aux->a_full[sa]);
-      }
-      ++gc;
-      if (++ckb == a.tpr) {
-        ckb = 0;
-        citem += gridDim.x;
-      }
+      if (lane == 0) mbar_arrive(&aux->out);
+      return warp_wait(&aux->out, n_sync++ & 1u, aux, p);
     };
-
-    convert();
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++n_items) {
       const Tile t = tile_at(p, pre, item);
-      const int h = t.n / 2, bufs = r_bufs(t.n);
-      float F[128];
+      const int cols = t.n / kSets;
+      const float* wout = p.wout + ((int64_t)blockIdx.x * 2 + (n_items & 1u)) * kMaxOut * kRows + my_row;
+      f32x2 F[kCols / 2];  // this row's sums, two tokens each
 #pragma unroll
-      for (int i = 0; i < 128; ++i) F[i] = 0.0f;
-      for (int kb = 0; kb < a.tpr; ++kb, ++gp) {
-        // (the last group's successor belongs to the next tile, whose outlier
-        // weights may only be written once this tile's are used)
-        if (kb + 1 < a.tpr) convert();
-        const int b = kb % bufs;
-        if (ok)
-          ok = wait_or_abort(&aux->a_full[gp % kAStages], (gp / kAStages) & 1u, aux, p) &&  // (the scales)
-               wait_or_abort(&aux->accf[half][b], (accp >> b) & 1u, aux, p);
-        ok = __all_sync(0xffffffffu, ok);
+      for (int i = 0; i < kCols / 2; ++i) F[i] = 0ull;
+      // this row's group scales, two groups ahead
+      const float* sp = a.scale + (int64_t)(t.rb0 + min(my_row >> 4, t.blocks - 1)) * a.tpr * kTileRows + (my_row & 15);
+      float s_next[2] = {__ldg(sp), a.tpr > 1 ? __ldg(sp + kTileRows) : 0.0f};
+      for (int kb = 0; kb < a.tpr; ++kb, ++g) {
+        const int b = (int)(g & 1u);
+        const float s1 = s_next[0];
+        s_next[0] = s_next[1];
+        s_next[1] = kb + 2 < a.tpr ? __ldg(sp + (kb + 2) * kTileRows) : 0.0f;
+        ok = warp_wait(&aux->accf[b], (g >> 1) & 1u, aux, p);
         if (!ok) break;
-        accp ^= 1u << b;
         fence_after();
-        const float s = aux->scale[gp % kScaleSlots][my_row];
-        const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + kTokens + 128 * half + b * h;
+        const f32x2 s = pack2(s1, s1);
+        const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + kTokens + kTokens * b + cols * set;
+        tmem_pieces(src, cols, [&](int c, const int(&r)[16]) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if (16 * c < h) {
-            int r[16];
-            tmem_ld16(src + 16 * c, r);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) F[16 * c + i] = fmaf(s, small_int_to_float(r[i]), F[16 * c + i]);
-          }
-        }
+          for (int i = 0; i < 8; ++i) F[8 * c + i] = fma2(s, pack2((float)r[2 * i], (float)r[2 * i + 1]), F[8 * c + i]);
+        });
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&aux->acce[half][b]);
+        if (lane == 0) mbar_arrive(&aux->acce[b]);
       }
       if (!ok) break;
-      ok = __all_sync(0xffffffffu, wait_or_abort(&aux->t_full, n_items & 1u, aux, p));
+      ok = warp_wait(&aux->t_full, n_items & 1u, aux, p) && warp_wait(&aux->wo_full, n_items & 1u, aux, p);
       if (!ok) break;
       fence_after();
       const int row = t.row0 + my_row;
       const bool live = my_row < t.blocks * kTileRows && row < a.N;
       const float al = __ldg(a.alpha + (int64_t)t.rb0 * kTileRows + min(my_row, t.blocks * kTileRows - 1));
-      const int t0 = half * h;                  // this half's tokens in the tile
-      const int nt = max(0, min(h, t.cnt - t0));
+      const int t0 = set * cols;                // this warp's tokens in the tile
+      const int nt = max(0, min(cols, t.cnt - t0));
+      const f32x2 al2 = pack2(al, al);
+      tmem_pieces(tmem + ((uint32_t)(32 * q) << 16) + t0, cols, [&](int c, const int(&r)[16]) {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        if (16 * c < h) {
-          int r[16];
-          tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + t0 + 16 * c, r);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float sx = __ldg(p.sxp + t.p0 + min(t0 + 16 * c + i, t.cnt - 1));
-            F[16 * c + i] = sx * fmaf(al, (float)r[i], F[16 * c + i]);
-          }
-        }
-      }
+        for (int i = 0; i < 8; ++i)
+          F[8 * c + i] = fma2(al2, pack2((float)r[2 * i], (float)r[2 * i + 1]), F[8 * c + i]);
+      });
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&aux->t_empty);
-      // the tile's outlier weights: written by every warp, then used, before the
-      // next tile's are written
-      __threadfence_block();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&aux->wo_full);
-      ok = __all_sync(0xffffffffu, wait_or_abort(&aux->wo_full, n_items & 1u, aux, p));
-      if (!ok) break;
-      const float* xo = p.xop + (int64_t)(t.p0 + t0) * p.n8;
-      for (int o0 = 0; o0 < n_out; o0 += 4) {
-        float w[4];
+      // the tile's token scales, then its outlier channels, kOutPass at a time, through
+      // shared memory: one row of 256 tokens each; this row's weights in registers
+      for (int o0 = -1; o0 < n_out; o0 += o0 < 0 ? 1 : kOutPass) {
+        const int no = o0 < 0 ? 1 : min(kOutPass, n_out - o0);
+        ok = out_sync();  // the rows of the pass before are used
+        if (!ok) break;
+        const float* src = o0 < 0 ? p.sxp : p.xop + (int64_t)o0 * a.n;
+        {
+          const int k = (int)threadIdx.x - 128 - 32 * kOperandWarps;  // a token per thread
+          static_assert(kPromoteThreads >= kTokens, "a token per thread");
+          float v[kOutPass];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          w[u] = o0 + u < n_out ? *reinterpret_cast<volatile float*>(wout + (o0 + u) * kRows + my_row) : 0.0f;
+          for (int o = 0; o < kOutPass; ++o)
+            v[o] = o < no && k < t.cnt ? __ldg(src + (int64_t)o * a.n + t.p0 + k) : 0.0f;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          if (8 * c < nt) {
+          for (int o = 0; o < kOutPass; ++o)
+            if (o < no && k < kTokens) xo[o * kTokens + k] = v[o];
+        }
+        float w[kOutPass];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int4 x = ldg_nc_v4(xo + (int64_t)min(8 * c + i, nt - 1) * p.n8 + o0);
-              float f = F[8 * c + i];
-              f = fmaf(w[3], __int_as_float(x.w), f);
-              f = fmaf(w[2], __int_as_float(x.z), f);
-              f = fmaf(w[1], __int_as_float(x.y), f);
-              F[8 * c + i] = fmaf(w[0], __int_as_float(x.x), f);
+        for (int o = 0; o < kOutPass; ++o) w[o] = o0 >= 0 && o < no ? wout[(o0 + o) * kRows] : 0.0f;
+        ok = out_sync();
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < kPieces; ++c) {
+          if (16 * c >= cols) break;
+          const ulonglong2* xr = reinterpret_cast<const ulonglong2*>(xo + t0 + 16 * c);
+          if (o0 < 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const ulonglong2 x = xr[i];
+              F[8 * c + 2 * i] = mul2(F[8 * c + 2 * i], x.x);
+              F[8 * c + 2 * i + 1] = mul2(F[8 * c + 2 * i + 1], x.y);
+            }
+          } else {
+#pragma unroll
+            for (int o = 0; o < kOutPass; ++o) {
+              if (o >= no) break;
+              const f32x2 w2 = pack2(w[o], w[o]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const ulonglong2 x = xr[o * (kTokens / 4) + i];
+                F[8 * c + 2 * i] = fma2(w2, x.x, F[8 * c + 2 * i]);
+                F[8 * c + 2 * i + 1] = fma2(w2, x.y, F[8 * c + 2 * i + 1]);
+              }
             }
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&aux->wo_empty);
+      if (!ok) break;
       if (live) {
         float* yr = a.y + (int64_t)(t.p0 + t0) * a.N + row;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * c + i < nt) yr[(int64_t)(32 * c + i) * a.N] = F[32 * c + i];
+        for (int i = 0; i < kCols / 2; ++i) {
+          const float2 v = unpack2(F[i]);
+          if (2 * i < nt) yr[(int64_t)(2 * i) * a.N] = v.x;
+          if (2 * i + 1 < nt) yr[(int64_t)(2 * i + 1) * a.N] = v.y;
         }
       }
-      ok = __all_sync(0xffffffffu, wait_or_abort(&aux->wo_empty, n_items & 1u, aux, p));
-      convert();  // the next tile's first group
     }
   }
   fence_before();
@@ -537,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Before the tiles: each place's activation codes (GATHER: rows in place order for
 // the TMA), scale and outlier values, one warp per place.
 template <bool GATHER>
-__global__ void __launch_bounds__(256) k_grouped_rows(const GroupedArgs a, int8_t* xs, float* sxp, float* xop, int n8) {
+__global__ void __launch_bounds__(256) k_grouped_rows(const GroupedArgs a, int8_t* xs, float* sxp, float* xop) {
   const int lane = threadIdx.x & 31;
   if (a.pdl) pdl_wait();
   pdl_launch_dependents();
@@ -558,7 +652,7 @@ __global__ void __launch_bounds__(256) k_grouped_rows(const GroupedArgs a, int8_
       for (int i = lane; i < a.xs / 16; i += 32) dst[i] = __ldg(src + i);
     }
     if (lane == 0) sxp[p] = __ldg(a.sx + r);
-    for (int i = lane; i < n8; i += 32) xop[(int64_t)p * n8 + i] = i < a.n_out ? __ldg(a.xout + (int64_t)r * a.n_out + i) : 0.0f;
+    for (int i = lane; i < a.n_out; i += 32) xop[(int64_t)i * a.n + p] = __ldg(a.xout + (int64_t)r * a.n_out + i);
   }
 }
 
@@ -576,23 +670,23 @@ Carve carve(int K, int64_t n, int sm_count) {
   c.xs = take((size_t)n * xq_stride_of(K));
   c.sxp = take((size_t)n * 4);
   c.xop = take((size_t)n * kMaxOut * 4);
-  c.wout = take((size_t)sm_count * kMaxOut * kRows * 4);
+  c.wout = take((size_t)sm_count * 2 * kMaxOut * kRows * 4);
   c.total = off;
   return c;
 }
 
 template <bool MASK>
-cudaError_t launch_tiles(const CUtensorMap& mb, Params p, int grid, cudaStream_t stream) {
-  p.off_b = kAStages * 2 * kABytes;
-  p.off_raw = p.off_b + kBStages * kBBytes;
-  p.off_aux = (int)round_up(p.off_raw + kRawStages * Raw<MASK>::kBytes, 16);
+cudaError_t launch_tiles(const CUtensorMap& mb, const WeightMaps& wm, Params p, int grid, cudaStream_t stream) {
+  p.off_raw = kStages * kStageBytes;
+  p.off_xo = p.off_raw + kRawStages * Raw<MASK>::kBytes;
+  p.off_aux = p.off_xo + kOutPass * kTokens * 4;
   p.off_pre = p.off_aux + (int)round_up(sizeof(Aux), 16);
   p.off_ostart = p.off_pre + (int)round_up(4 * (p.a.E + 1), 16);
   const int smem = p.off_ostart + (int)round_up(4 * (p.a.tpr + 1), 16) + 1024;
   if (smem > 227 * 1024) return cudaErrorInvalidValue;
   auto* fn = k_grouped_tc5<MASK>;
   // the register split of the warpgroups must add up to the launch's registers
-  static_assert(128 * kProducerRegs + kComputeThreads * kComputeRegs == kThreads * kLaunchRegs, "register split");
+  static_assert(128 * kProducerRegs + 32 * kOperandWarps * kOperandRegs + kPromoteThreads * kPromoteRegs <= kThreads * kLaunchRegs, "register split");
   static const bool regs_ok = [&] {
     cudaFuncAttributes at;
     return cudaFuncGetAttributes(&at, fn) == cudaSuccess && at.numRegs == kLaunchRegs;
@@ -610,7 +704,7 @@ cudaError_t launch_tiles(const CUtensorMap& mb, Params p, int grid, cudaStream_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, mb, p);
+  return cudaLaunchKernelEx(&cfg, fn, mb, wm, p);
 }
 
 }  // namespace
@@ -631,7 +725,6 @@ cudaError_t launch_grouped_tc5(const GroupedArgs& a, void* workspace, int sm_cou
   float* xop = reinterpret_cast<float*>(w + c.xop);
   p.sxp = sxp;
   p.xop = xop;
-  p.n8 = (int)round_up(std::max(a.n_out, 1), 4);
   p.wout = reinterpret_cast<float*>(w + c.wout);
   p.rt = (int)ceil_div(a.rbe, kBlocks);
   // rows of the activation map: the places (in place order already without an
@@ -639,7 +732,16 @@ cudaError_t launch_grouped_tc5(const GroupedArgs& a, void* workspace, int sm_cou
   CUtensorMap mb;
   const int64_t rows = a.order ? a.n : std::min(a.n, a.rows);
   if (!tc05::make_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.order ? xs : a.xq, (uint64_t)a.xs, (uint64_t)rows,
-                      (uint64_t)a.xs, kTileK, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+                      (uint64_t)a.xs, kTileK, kTokenUnit, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  WeightMaps wm;
+  const uint64_t blocks = (uint64_t)a.E * a.rbe;
+  auto weight_map = [&](CUtensorMap* m, const void* base, int tile_bytes) {  // 8-byte elements
+    return tc05::make_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, base, (uint64_t)a.tpr * tile_bytes / 8, blocks,
+                          (uint64_t)a.tpr * tile_bytes, tile_bytes / 8, kBlocks, CU_TENSOR_MAP_SWIZZLE_NONE);
+  };
+  if (!weight_map(&wm.codes, a.res, 2048) || !weight_map(&wm.sign, a.sign, 256) ||
+      !weight_map(&wm.mask, a.mask ? a.mask : a.sign, 256))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min<int64_t>(ceil_div(a.n, 8), 4 * sm_count));
@@ -650,13 +752,13 @@ cudaError_t launch_grouped_tc5(const GroupedArgs& a, void* workspace, int sm_cou
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.pdl ? 1 : 0;
-  const cudaError_t e = a.order ? cudaLaunchKernelEx(&cfg, k_grouped_rows<true>, a, xs, sxp, xop, p.n8)
-                                : cudaLaunchKernelEx(&cfg, k_grouped_rows<false>, a, xs, sxp, xop, p.n8);
+  const cudaError_t e = a.order ? cudaLaunchKernelEx(&cfg, k_grouped_rows<true>, a, xs, sxp, xop)
+                                : cudaLaunchKernelEx(&cfg, k_grouped_rows<false>, a, xs, sxp, xop);
   if (e != cudaSuccess) return e;
   const int64_t tiles = std::min<int64_t>(a.n, a.E + a.n / kTokens) * p.rt;
   if (tiles >= INT32_MAX) return cudaErrorInvalidValue;
   const int grid = (int)std::min<int64_t>(tiles, sm_count);
-  return a.mask ? launch_tiles<true>(mb, p, grid, stream) : launch_tiles<false>(mb, p, grid, stream);
+  return a.mask ? launch_tiles<true>(mb, wm, p, grid, stream) : launch_tiles<false>(mb, wm, p, grid, stream);
 }
 
 }  // namespace sq
