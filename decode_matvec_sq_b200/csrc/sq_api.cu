@@ -710,6 +710,7 @@ sq_status sq_grouped_linear(const sq_packed_weight* stack, int32_t E, int32_t N,
   if (st != SQ_OK) return st;
   if (!xq || !sx || !offsets || !y) return SQ_ERR_INVALID_ARG;
   if (rows < 1 || rows > kMaxEntries || n < 1 || n > kMaxEntries || div < 1) return SQ_ERR_SHAPE;
+  if ((int64_t)n * (tiles_rows(N) / kTileRows) >= (1ll << 40) / (tiles_cols(stack->K) / kTileK)) return SQ_ERR_SHAPE;
   if (n_out < 0 || n_out > kMaxOutliers || n_out > stack->K) return SQ_ERR_SHAPE;
   if (n_out > 0 && (!idx || !x_out)) return SQ_ERR_INVALID_ARG;
   if (flags & ~SQ_LAUNCH_PDL) return SQ_ERR_INVALID_ARG;

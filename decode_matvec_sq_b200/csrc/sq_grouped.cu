@@ -13,8 +13,9 @@
 // the decode kernel of one weight splits its own.  Nothing is read for an expert
 // without tokens, and the host needs no counts: every CTA forms the groups from
 // the device's offsets.
-// What bounds it: the weight stream.  Each warp keeps D tiles (2.3 KB each) in
-// flight by bulk copies into its shared-memory ring, one mbarrier per slot.
+// What bounds it: the weight stream.  Each warp keeps 2 D tiles (2.3 KB each) in
+// flight by bulk copies into its shared-memory ring, two tiles to a slot, one
+// mbarrier per slot.
 // The trunk operand is +-1 (0 outside the mask) bytes made from the bits by one
 // shift, one sign-replicating byte permute and one three-input logic operation
 // per four channels, so T needs one MMA where bits as 0/-1 need two.
@@ -32,21 +33,24 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxDepth = 4;
+constexpr int kMaxDepth = 3;
+constexpr int kPair = 2;   // tiles per ring slot: neighbours in memory, copied together
 
 struct Params {
   GroupedArgs a;
   int depth;
-  int off_ring, off_part, off_pre, off_ostart;  // shared-memory offsets (bytes)
+  int off_ring, off_part, off_pre, off_ostart, off_idx;  // shared-memory offsets (bytes)
 };
 
+// One ring slot: kPair tiles, array by array.
 template <bool MASK, bool ASYM>
 struct Slot {
-  static constexpr int kSign = 2048;
-  static constexpr int kMask = kSign + 256;
-  static constexpr int kScale = MASK ? kMask + 256 : kMask;
-  static constexpr int kZero = kScale + 64;
-  static constexpr int kBytes = ASYM ? kZero + 64 : kZero;
+  static constexpr int kSign = kPair * 2048;
+  static constexpr int kMask = kSign + kPair * 256;
+  static constexpr int kScale = MASK ? kMask + kPair * 256 : kMask;
+  static constexpr int kZero = kScale + kPair * 64;
+  static constexpr int kTile = 2048 + 256 + 64 + (MASK ? 256 : 0) + (ASYM ? 64 : 0);
+  static constexpr int kBytes = kPair * kTile;
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -81,30 +85,25 @@ __device__ __forceinline__ uint32_t swap_halves(uint32_t b) {
   return ((b >> 4) & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
 }
 
-// The tokens of one group as a lane sees them.
+// The tokens of one group: lane l holds those of token l % (8 NT).
 template <int NT>
 struct Tokens {
   const int8_t* x[NT];   // this lane's B column (token gid of each eight), at its 32 channels
-  float sx[NT][2];       // accumulator columns 2 tid4, 2 tid4 + 1
-  int xo[NT][2];         // their rows of x_out
+  int row;               // activation row and scale of token l
+  float sx;
   int p0, cnt;           // first place, tokens
 };
 
 template <int NT>
-__device__ __forceinline__ void load_tokens(Tokens<NT>& tk, const GroupedArgs& a, int p0, int cnt, int gid, int tid4) {
+__device__ __forceinline__ void load_tokens(Tokens<NT>& tk, const GroupedArgs& a, int p0, int cnt, int lane) {
   tk.p0 = p0;
   tk.cnt = cnt;
+  // (columns past the group repeat its last token; they are not written)
+  tk.row = source_row(a, p0 + min(lane & (8 * NT - 1), cnt - 1));
+  tk.sx = __ldg(a.sx + tk.row);
 #pragma unroll
-  for (int g = 0; g < NT; ++g) {
-    // columns past the group repeat its last token; they are not written
-    tk.x[g] = a.xq + (int64_t)source_row(a, p0 + min(gid + 8 * g, cnt - 1)) * a.xs + tid4 * 32;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int r = source_row(a, p0 + min(2 * tid4 + c + 8 * g, cnt - 1));
-      tk.sx[g][c] = __ldg(a.sx + r);
-      tk.xo[g][c] = r;
-    }
-  }
+  for (int g = 0; g < NT; ++g)
+    tk.x[g] = a.xq + (int64_t)__shfl_sync(0xffffffffu, tk.row, (lane >> 2) + 8 * g) * a.xs + (lane & 3) * 32;
 }
 
 template <bool MASK, bool ASYM, int NT>
@@ -114,81 +113,146 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps * kMaxDepth];
   __shared__ int part_i[kWarps];
-  __shared__ int bad_idx;
   const GroupedArgs& a = p.a;
   float* part = reinterpret_cast<float*>(smem + p.off_part);  // [kWarps][2][16][TG]
   int* pre = reinterpret_cast<int*>(smem + p.off_pre);
   int* ostart = reinterpret_cast<int*>(smem + p.off_ostart);  // first outlier of each channel group
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* idx_s = reinterpret_cast<int*>(smem + p.off_idx);
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int gid = lane >> 2, tid4 = lane & 3;
   const int D = p.depth;
 
   if (lane == 0)
     for (int d = 0; d < D; ++d) mbar_init(&bars[warp * kMaxDepth + d], 1);
   fence_barrier_init();
-  if (threadIdx.x == 0) bad_idx = 0;
-  __syncthreads();
-  // the outlier list (fixed once a layer is set up), before the wait
-  for (int i = threadIdx.x; i < a.n_out; i += kThreads) {
-    const int j = __ldg(a.idx + i), jp = i > 0 ? __ldg(a.idx + i - 1) : -1;
-    if (j < 0 || j >= a.K || jp >= j) bad_idx = 1;
+  if (!a.pdl) pdl_wait();
+  // the outlier list (with SQ_LAUNCH_PDL fixed, and read before the wait)
+  const int i0 = threadIdx.x;
+  const int jv = i0 < a.n_out ? __ldg(a.idx + i0) : 0, jp = i0 > 0 && i0 < a.n_out ? __ldg(a.idx + i0 - 1) : -1;
+  if (a.pdl) pdl_wait();
+  pdl_launch_dependents();
+  // Segments: with at most 32 experts every warp keeps expert `lane`'s in registers
+  // (no barrier before the first copies), else the CTA forms them in shared memory.
+  const bool few = a.E <= 32;
+  int2 seg = make_int2(0, 0);
+  int first = 0, groups;
+  if (few) {
+    if (lane < a.E) seg = segment_bounds(a.offsets, a.n, lane, a.status);
+    const int v = (seg.y - seg.x + TG - 1) / TG;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    first = incl - v;
+    groups = __shfl_sync(0xffffffffu, incl, 31);
+  } else {
+    groups = segment_units<kThreads>(a.offsets, a.E, a.n, a.status, TG, pre, part_i);
   }
-  __syncthreads();
-  const int n_out = bad_idx ? 0 : a.n_out;
-  if (bad_idx && threadIdx.x == 0) set_status(a.status, SQ_ERR_INVALID_ARG);
-  for (int i = threadIdx.x; i < n_out; i += kThreads) {
-    const int g0 = i > 0 ? (__ldg(a.idx + i - 1) >> 7) + 1 : 0, g1 = __ldg(a.idx + i) >> 7;
-    for (int g = g0; g <= g1; ++g) ostart[g] = i;
-  }
-  for (int g = (n_out > 0 ? (__ldg(a.idx + n_out - 1) >> 7) + 1 : 0) + threadIdx.x; g <= a.tpr; g += kThreads)
-    ostart[g] = n_out;
-  if (a.pdl) {
-    pdl_wait();
-    pdl_launch_dependents();
-  }
-  const int groups = segment_units<kThreads>(a.offsets, a.E, a.n, a.status, TG, pre, part_i);
+  // expert of group u, its first group and its places
+  struct Group {
+    int e, first;
+    int2 seg;
+  };
+  auto group_at = [&](int u) -> Group {
+    Group g;
+    if (few) {
+      g.e = 31 - __clz(__ballot_sync(0xffffffffu, lane < a.E && first <= u));
+      g.first = __shfl_sync(0xffffffffu, first, g.e);
+      g.seg = make_int2(__shfl_sync(0xffffffffu, seg.x, g.e), __shfl_sync(0xffffffffu, seg.y, g.e));
+    } else {
+      g.e = unit_expert(pre, a.E, u);
+      g.first = pre[g.e];
+      g.seg = segment_bounds(a.offsets, a.n, g.e, nullptr);
+    }
+    return g;
+  };
 
-  // the CTA's (group, row block) pairs: the fewest CTAs with the largest share
-  // that one CTA per SM gives
+  // the CTA's (group, row block) pairs: the largest share that one CTA per SM
+  // gives for as many CTAs as it takes, so that no CTA finishes alone
   const int64_t V = (int64_t)groups * a.rbe;
-  if (V == 0) return;
-  const int64_t share = (V + gridDim.x - 1) / gridDim.x, used = (V + share - 1) / share;
-  if ((int64_t)blockIdx.x >= used) return;
-  const int64_t v0 = blockIdx.x * V / used, v1 = (blockIdx.x + 1) * V / used;
-  const int64_t T0 = v0 * a.tpr, T1 = v1 * a.tpr, len = T1 - T0;
-  const int64_t t0 = T0 + warp * len / kWarps, t1 = T0 + (warp + 1) * len / kWarps;
+  const int64_t share = fast_div(V + gridDim.x - 1, (int)gridDim.x), v0 = blockIdx.x * share;
+  if (v0 >= V) return;
+  const int len = (int)min(share, V - v0) * a.tpr;  // tiles (the host keeps it in 32 bits)
+  const int t0 = (int)(((int64_t)warp * len) >> 4), t1 = (int)(((int64_t)(warp + 1) * len) >> 4);
+  static_assert(kWarps == 16, "the split over the warps");
+  // this warp's first tile: row block rb of the expert of group u, channel group cg
+  const int lrb0 = t0 / a.tpr;
+  int cg = t0 - lrb0 * a.tpr, u = (int)fast_div(v0 + lrb0, a.rbe), rb = (int)(v0 + lrb0 - (int64_t)u * a.rbe);
+  Group grp = group_at(min(u, groups - 1));
+  const int per_group = a.rbe * a.tpr;
 
   // producer cursor: the next tile to copy
   uint8_t* ring = smem + p.off_ring + warp * D * SL::kBytes;
   const uint32_t ring_u = smem_u32(ring), bar_u = smem_u32(&bars[warp * kMaxDepth]);
-  int64_t ct = t0, ctile = 0;  // virtual tile, tile in the stack
-  int cleft = 0;               // tiles left in the cursor's group
-  auto seek = [&](int64_t t) {
-    const int64_t vrb = t / a.tpr;
-    const int u = (int)(vrb / a.rbe), e = unit_expert(pre, a.E, u);
-    ctile = ((int64_t)e * a.rbe + vrb % a.rbe) * a.tpr + t % a.tpr;
-    cleft = (int)((int64_t)(u + 1) * a.rbe * a.tpr - t);
-  };
+  int ct = t0, cu = u, cleft = per_group - rb * a.tpr - cg;  // tile; group, its tiles left
+  int64_t ctile = (int64_t)grp.e * per_group + rb * a.tpr + cg;  // tile in the stack
+  // the next slot: kPair tiles, or one at the end of a group or of the range
   auto copy = [&](int slot) {
     if (ct >= t1) return;
-    if (cleft == 0) seek(ct);
+    if (cleft == 0) {
+      ctile = (int64_t)group_at(++cu).e * per_group;
+      cleft = per_group;
+    }
+    const uint32_t c = cleft >= kPair && ct + kPair <= t1 ? kPair : 1;
     const uint32_t dst = ring_u + slot * SL::kBytes, bar = bar_u + 8 * slot;
-    if (lane == 0) mbar_arrive_expect_tx(&bars[warp * kMaxDepth + slot], SL::kBytes);
+    if (elect_one()) {
+      mbar_arrive_expect_tx(&bars[warp * kMaxDepth + slot], c * SL::kTile);
+      bulk_load(dst, a.res + ctile * 2048, c * 2048, bar);
+      bulk_load(dst + SL::kSign, a.sign + ctile * 64, c * 256, bar);
+      bulk_load(dst + SL::kScale, a.scale + ctile * 16, c * 64, bar);
+      if (MASK) bulk_load(dst + SL::kMask, a.mask + ctile * 64, c * 256, bar);
+      if (ASYM) bulk_load(dst + SL::kZero, a.zero + ctile * 16, c * 64, bar);
+    }
     __syncwarp();
-    if (lane == 0) bulk_load(dst, a.res + ctile * 2048, 2048, bar);
-    if (lane == 1) bulk_load(dst + SL::kSign, a.sign + ctile * 64, 256, bar);
-    if (lane == 2) bulk_load(dst + SL::kScale, a.scale + ctile * 16, 64, bar);
-    if (MASK && lane == 3) bulk_load(dst + SL::kMask, a.mask + ctile * 64, 256, bar);
-    if (ASYM && lane == 4) bulk_load(dst + SL::kZero, a.zero + ctile * 16, 64, bar);
-    ++ct;
-    ++ctile;
-    --cleft;
+    ct += c;
+    ctile += c;
+    cleft -= c;
   };
+  // the group's tokens and the row block's scales
+  Tokens<NT> tk;
+  int64_t erow = 0;  // first row of the expert in the stack
+  int gleft = 0;     // tiles left in the group
+  float al[2] = {0.0f, 0.0f};
+  auto enter_group = [&] {
+    const int p0 = grp.seg.x + (u - grp.first) * TG;
+    load_tokens<NT>(tk, a, p0, min(TG, grp.seg.y - p0), lane);
+    erow = (int64_t)grp.e * a.rbe * kTileRows;
+  };
+  auto enter_rows = [&] {
+    al[0] = __ldg(a.alpha + erow + rb * kTileRows + gid);
+    al[1] = __ldg(a.alpha + erow + rb * kTileRows + gid + 8);
+  };
+  if (t0 < t1) {
+    gleft = per_group - rb * a.tpr - cg;
+    // (before the copies, whose queue these small loads would stand in)
+    enter_group();
+    enter_rows();
+  }
   for (int d = 0; d < D; ++d) copy(d);
+
+  // the outlier tables, while the first tiles are on their way
+  bool bad = i0 < a.n_out && (jv < 0 || jv >= a.K || jp >= jv);
+  for (int i = i0 + kThreads; i < a.n_out; i += kThreads) {
+    const int j = __ldg(a.idx + i);
+    bad |= j < 0 || j >= a.K || __ldg(a.idx + i - 1) >= j;
+  }
+  const int n_out = __syncthreads_or(bad) ? 0 : a.n_out;
+  if (n_out < a.n_out && threadIdx.x == 0) set_status(a.status, SQ_ERR_INVALID_ARG);
+  for (int i = i0; i < n_out; i += kThreads) {
+    const int j = i < kThreads ? jv : __ldg(a.idx + i), jq = i == 0 ? -1 : i < kThreads ? jp : __ldg(a.idx + i - 1);
+    idx_s[i] = j;
+    for (int g = i > 0 ? (jq >> 7) + 1 : 0; g <= (j >> 7); ++g) ostart[g] = i;
+    if (i == n_out - 1)
+      for (int g = (j >> 7) + 1; g <= a.tpr; ++g) ostart[g] = n_out;
+  }
+  if (n_out == 0)
+    for (int g = threadIdx.x; g <= a.tpr; g += kThreads) ostart[g] = 0;
+  __syncthreads();
 
   const bool hi = tid4 >= 2;  // takes its code words in the order 2, 3, 0, 1
   const int cofs = lane * 64 + (hi ? 32 : 0), xofs = hi ? 16 : 0;
-  Tokens<NT> tk;
   int T[NT][4];
   float F[NT][4], U[NT][4];
   auto clear = [&] {
@@ -201,30 +265,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
       }
   };
   clear();
-  int64_t vrb = t0 / a.tpr;
-  int cg = (int)(t0 - vrb * a.tpr), rb = 0;  // channel group; row block in the expert
-  int64_t erow = 0;                                         // first row of the expert in the stack
-  float al[2] = {0.0f, 0.0f};
   bool head = cg == 0, timed_out = false;
-  int slot = 0;
+  int slot = 0, sub = 0, in_slot = 0;  // tile of the slot, tiles in it
   uint32_t phase = 0;
 
-  // group and row block of virtual row block v
-  auto enter = [&](int64_t v, bool new_group) {
-    if (new_group) {
-      const int u = (int)(v / a.rbe), e = unit_expert(pre, a.E, u);
-      const int2 b = segment_bounds(a.offsets, a.n, e, a.status);
-      const int p0 = b.x + (u - pre[e]) * TG;
-      load_tokens<NT>(tk, a, p0, min(TG, b.y - p0), gid, tid4);
-      rb = (int)(v - (int64_t)u * a.rbe);
-      erow = (int64_t)e * a.rbe * kTileRows;
-    }
-    al[0] = __ldg(a.alpha + erow + rb * kTileRows + gid);
-    al[1] = __ldg(a.alpha + erow + rb * kTileRows + gid + 8);
-  };
-  if (t0 < t1) enter(vrb, true);
-
-  for (int64_t t = t0; t < t1; ++t) {
+  for (int t = t0; t < t1; ++t) {
     // activation words of this tile (the copies may still be on their way)
     uint32_t xw[NT][8];
 #pragma unroll
@@ -234,24 +279,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
       xw[g][0] = u.x; xw[g][1] = u.y; xw[g][2] = u.z; xw[g][3] = u.w;
       xw[g][4] = v.x; xw[g][5] = v.y; xw[g][6] = v.z; xw[g][7] = v.w;
     }
-    const bool landed = mbar_wait(&bars[warp * kMaxDepth + slot], (phase >> slot) & 1u);
-    if (!__all_sync(0xffffffffu, landed)) {
-      timed_out = true;
-      break;
+    const int o0 = ostart[cg], o1 = ostart[cg + 1];
+    float xf[NT][2];  // the first outlier channel's activations, if the tile has one
+#pragma unroll
+    for (int g = 0; g < NT; ++g)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = __shfl_sync(0xffffffffu, tk.row, 2 * tid4 + c + 8 * g);
+        xf[g][c] = o0 < o1 ? __ldg(a.xout + (int64_t)r * a.n_out + o0) : 0.0f;
+      }
+    if (sub == 0) {
+      const bool landed = mbar_wait(&bars[warp * kMaxDepth + slot], (phase >> slot) & 1u);
+      if (!__all_sync(0xffffffffu, landed)) {
+        timed_out = true;
+        break;
+      }
+      phase ^= 1u << slot;
+      in_slot = gleft >= kPair && t + kPair <= t1 ? kPair : 1;
     }
-    phase ^= 1u << slot;
+    --gleft;
     const uint8_t* sl = ring + slot * SL::kBytes;
+    const uint8_t* ql = sl + sub * 2048;
+    const uint8_t* bl = sl + SL::kSign + sub * 256;
+    const uint8_t* ml = sl + SL::kMask + sub * 256;
     uint32_t q[4][4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      const uint4 v = *reinterpret_cast<const uint4*>(sl + ((cofs ^ ((m & 2) << 4)) + (m & 1) * 16));
+      const uint4 v = *reinterpret_cast<const uint4*>(ql + ((cofs ^ ((m & 2) << 4)) + (m & 1) * 16));
       q[m][0] = v.x; q[m][1] = v.y; q[m][2] = v.z; q[m][3] = v.w;
     }
-    uint2 s = *reinterpret_cast<const uint2*>(sl + SL::kSign + lane * 8);
+    uint2 s = *reinterpret_cast<const uint2*>(bl + lane * 8);
     uint2 k = make_uint2(0u, 0u);
-    if constexpr (MASK) k = *reinterpret_cast<const uint2*>(sl + SL::kMask + lane * 8);
-    const float c0 = *reinterpret_cast<const float*>(sl + SL::kScale + gid * 4);
-    const float c1 = *reinterpret_cast<const float*>(sl + SL::kScale + gid * 4 + 32);
+    if constexpr (MASK) k = *reinterpret_cast<const uint2*>(ml + lane * 8);
+    const float c0 = *reinterpret_cast<const float*>(sl + SL::kScale + sub * 64 + gid * 4);
+    const float c1 = *reinterpret_cast<const float*>(sl + SL::kScale + sub * 64 + gid * 4 + 32);
     if (hi) {
       s.x = swap_halves(s.x);
       s.y = swap_halves(s.y);
@@ -286,8 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
     }
     int z0 = 0, z1 = 0;
     if constexpr (ASYM) {
-      z0 = *reinterpret_cast<const int*>(sl + SL::kZero + gid * 4);
-      z1 = *reinterpret_cast<const int*>(sl + SL::kZero + gid * 4 + 32);
+      z0 = *reinterpret_cast<const int*>(sl + SL::kZero + sub * 64 + gid * 4);
+      z1 = *reinterpret_cast<const int*>(sl + SL::kZero + sub * 64 + gid * 4 + 32);
     }
 #pragma unroll
     for (int g = 0; g < NT; ++g)
@@ -303,15 +364,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
       }
     // outlier channels of this tile: the dequantized weight of the lane's two
     // rows from the slot, times its tokens' binary32 activations
-    for (int o = ostart[cg]; o < ostart[cg + 1]; ++o) {
-      const int j = __ldg(a.idx + o) & 127, w = (j & 31) >> 2;
+    for (int o = o0; o < o1; ++o) {
+      const int j = idx_s[o] & 127, w = (j & 31) >> 2;
       const int own = gid * 4 + (j >> 5);
-      const int8_t* cb = reinterpret_cast<const int8_t*>(sl) + own * 64 + (w >> 1) * 16 + (w & 1) * 8 + (j & 3);
-      const uint2 sb = *reinterpret_cast<const uint2*>(sl + SL::kSign + own * 8);
+      const int8_t* cb = reinterpret_cast<const int8_t*>(ql) + own * 64 + (w >> 1) * 16 + (w & 1) * 8 + (j & 3);
+      const uint2 sb = *reinterpret_cast<const uint2*>(bl + own * 8);
       const int bit = tiled_bit_of(j & 31);
       float w0 = ((sb.x >> bit) & 1u) ? al[0] : -al[0], w1 = ((sb.y >> bit) & 1u) ? al[1] : -al[1];
       if constexpr (MASK) {
-        const uint2 mb = *reinterpret_cast<const uint2*>(sl + SL::kMask + own * 8);
+        const uint2 mb = *reinterpret_cast<const uint2*>(ml + own * 8);
         w0 = ((mb.x >> bit) & 1u) ? w0 : 0.0f;
         w1 = ((mb.y >> bit) & 1u) ? w1 : 0.0f;
       }
@@ -319,17 +380,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
       w1 = fmaf(c1, (float)(cb[4] - z1), w1);
 #pragma unroll
       for (int g = 0; g < NT; ++g) {
-        const float x0 = __ldg(a.xout + (int64_t)tk.xo[g][0] * a.n_out + o);
-        const float x1 = __ldg(a.xout + (int64_t)tk.xo[g][1] * a.n_out + o);
+        const int r0 = __shfl_sync(0xffffffffu, tk.row, 2 * tid4 + 8 * g);
+        const int r1 = __shfl_sync(0xffffffffu, tk.row, 2 * tid4 + 1 + 8 * g);
+        const float x0 = o == o0 ? xf[g][0] : __ldg(a.xout + (int64_t)r0 * a.n_out + o);
+        const float x1 = o == o0 ? xf[g][1] : __ldg(a.xout + (int64_t)r1 * a.n_out + o);
         U[g][0] = fmaf(w0, x0, U[g][0]);
         U[g][1] = fmaf(w0, x1, U[g][1]);
         U[g][2] = fmaf(w1, x0, U[g][2]);
         U[g][3] = fmaf(w1, x1, U[g][3]);
       }
     }
-    __syncwarp();  // every lane has read the slot
-    copy(slot);
-    if (++slot == D) slot = 0;
+    if (++sub == in_slot) {
+      __syncwarp();  // every lane has read the slot
+      copy(slot);
+      if (++slot == D) slot = 0;
+      sub = 0;
+    }
 
     const bool row_end = cg == a.tpr - 1;
     if (row_end || t + 1 == t1) {
@@ -339,7 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int c = 2 * tid4 + (i & 1) + 8 * g, r = gid + (i >> 1) * 8;
-          const float v = fmaf(tk.sx[g][i & 1], fmaf(al[i >> 1], (float)T[g][i], F[g][i]), U[g][i]);
+          const float sx = __shfl_sync(0xffffffffu, tk.sx, c);
+          const float v = fmaf(sx, fmaf(al[i >> 1], (float)T[g][i], F[g][i]), U[g][i]);
           if (c < tk.cnt) {
             if (whole) {
               if (rb * kTileRows + r < a.N) a.y[(int64_t)(tk.p0 + c) * a.N + rb * kTileRows + r] = v;
@@ -352,9 +419,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
       clear();
       head = true;
       if (row_end && t + 1 < t1) {
-        ++vrb;
-        ++rb;
-        enter(vrb, rb == a.rbe);
+        if (++rb == a.rbe) {
+          rb = 0;
+          grp = group_at(++u);
+          gleft = per_group;
+          enter_group();
+        }
+        enter_rows();
       }
     }
     if (++cg == a.tpr) cg = 0;
@@ -368,11 +439,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
   if (t0 >= t1 || timed_out) return;
   // the row block that begins in this warp's range and ends past it: the later
   // warps' parts added in warp order
-  const int64_t last = (t1 - 1) / a.tpr;
-  if (last * a.tpr >= t0 && t1 % a.tpr != 0) {
-    const int64_t end = (last + 1) * a.tpr;
+  const int last = (t1 - 1) / a.tpr;
+  if (last * a.tpr >= t0 && t1 != (last + 1) * a.tpr) {
+    const int end = (last + 1) * a.tpr;
     int w_hi = warp;
-    while (w_hi + 1 < kWarps && T0 + (w_hi + 1) * len / kWarps < end) ++w_hi;
+    while (w_hi + 1 < kWarps && (int)(((int64_t)(w_hi + 1) * len) >> 4) < end) ++w_hi;
 #pragma unroll
     for (int g = 0; g < NT; ++g)
 #pragma unroll
@@ -381,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
         if (c >= tk.cnt) continue;
         float v = part[((warp * 2 + 1) * 16 + r) * TG + c];
         for (int w = warp + 1; w <= w_hi; ++w)
-          if (T0 + w * len / kWarps < T0 + (w + 1) * len / kWarps) v += part[((w * 2) * 16 + r) * TG + c];
+          if ((((int64_t)w * len) >> 4) < (((int64_t)(w + 1) * len) >> 4)) v += part[((w * 2) * 16 + r) * TG + c];
         if (rb * kTileRows + r < a.N) a.y[(int64_t)(tk.p0 + c) * a.N + rb * kTileRows + r] = v;
       }
   }
@@ -394,14 +465,15 @@ cudaError_t launch_nt(const GroupedArgs& a, int sm_count, cudaStream_t stream) {
   Params p;
   p.a = a;
   const int part = kWarps * 2 * 16 * TG * 4;
-  const int tables = (int)round_up(4 * (a.E + 1), 16) + (int)round_up(4 * (a.tpr + 1), 16);
+  const int tables = (int)round_up(4 * (a.E + 1), 16) + (int)round_up(4 * (a.tpr + 1), 16) + (int)round_up(4 * (a.n_out + 1), 16);
   constexpr int kMax = 227 * 1024 - 2048;
   p.depth = std::min(kMaxDepth, (kMax - part - tables) / (kWarps * SL::kBytes));
-  if (p.depth < 2) return cudaErrorInvalidValue;
+  if (p.depth < 1) return cudaErrorInvalidValue;
   p.off_ring = 0;
   p.off_part = kWarps * p.depth * SL::kBytes;
   p.off_pre = p.off_part + part;
   p.off_ostart = p.off_pre + (int)round_up(4 * (a.E + 1), 16);
+  p.off_idx = p.off_ostart + (int)round_up(4 * (a.tpr + 1), 16);
   const int smem = p.off_part + part + tables;
   auto* fn = k_grouped<MASK, ASYM, NT>;
   const cudaError_t e = ensure_smem_attr((const void*)fn, smem);
@@ -416,7 +488,9 @@ cudaError_t launch_nt(const GroupedArgs& a, int sm_count, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = a.pdl ? 1 : 0;
+  // (always: the kernel waits for the one before it, at its start or, with
+  // SQ_LAUNCH_PDL, after the outlier list; only its launch is brought forward)
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
@@ -429,7 +503,9 @@ cudaError_t launch_kind(const GroupedArgs& a, int sm_count, cudaStream_t stream)
 
 }  // namespace
 
-bool grouped_many(int E, int64_t n) { return n >= 24 * (int64_t)E; }
+// Measured crossover (8 experts 4096 x 4096: 51 us at 16, 80 us at 32 places per expert with the
+// few-token kernel, 75 and 81 us with the other; 4 experts 4096 -> 14336: 87 and 141, 137 and 141).
+bool grouped_many(int E, int64_t n) { return n >= 32 * (int64_t)E; }
 
 size_t grouped_workspace_bytes(int E, int K, int64_t n, bool asym, int sm_count) {
   return grouped_many(E, n) && !asym ? grouped_tc5_workspace_bytes(K, n, sm_count) : 0;
@@ -438,7 +514,10 @@ size_t grouped_workspace_bytes(int E, int K, int64_t n, bool asym, int sm_count)
 cudaError_t launch_grouped(const GroupedArgs& a, void* workspace, int sm_count, cudaStream_t stream) {
   if (grouped_many(a.E, a.n) && grouped_tc5_supported(a.n_out, a.zero != nullptr))
     return launch_grouped_tc5(a, workspace, sm_count, stream);
-  if (a.n <= 8) return launch_kind<1>(a, sm_count, stream);
+  // Groups of 8 tokens up to 4 places per expert, of 16 above: the second eight
+  // cost every tile 60 instructions, a second pass over the weights is rare at four
+  // (16 tokens top-2 of 8 experts 14336 -> 4096: 115 against 139 us).
+  if (a.n <= std::max(8, 4 * a.E)) return launch_kind<1>(a, sm_count, stream);
   return launch_kind<2>(a, sm_count, stream);
 }
 

@@ -36,6 +36,19 @@ struct GroupedArgs {
   int pdl;
 };
 
+// a / b for 0 <= a, 0 < b, in 32 bits where a allows it (a 64-bit division costs
+// hundreds of clocks, and the walks over the tiles begin with several).
+__device__ __forceinline__ int64_t fast_div(int64_t a, int b) {
+  if ((a >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(pred));
+  return pred != 0;
+}
+
 // Bounds of segment e of a sort of n entries, clamped to them (offsets that do
 // not ascend in [0, n] are reported; no access leaves the arrays).
 __device__ __forceinline__ int2 segment_bounds(const int32_t* offsets, int n, int e, int32_t* status) {
@@ -51,7 +64,8 @@ __device__ __forceinline__ int source_row(const GroupedArgs& p, int at) {
   int r = at;
   if (p.order) {
     r = __ldg(p.order + at);
-    r = r < 0 ? -1 : r / p.div;
+    // (the number of choices is mostly a power of two)
+    if (r > 0) r = (p.div & (p.div - 1)) == 0 ? r >> (__ffs(p.div) - 1) : r / p.div;
   }
   if (r < 0 || r >= p.rows) {
     set_status(p.status, SQ_ERR_INVALID_ARG);

@@ -130,11 +130,6 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Au
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Aux* aux, const Params& p) {
   return __all_sync(0xffffffffu, wait_or_abort(bar, parity, aux, p));
 }
-__device__ __forceinline__ bool elect_one() {
-  uint32_t pred;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(pred));
-  return pred != 0;
-}
 __device__ __forceinline__ bool aborted(const Aux* aux) {
   return *reinterpret_cast<const volatile int*>(&aux->abort) != 0;
 }

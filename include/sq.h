@@ -545,7 +545,8 @@ sq_status sq_expert_view(const sq_packed_weight *stack, int32_t E, int32_t N, in
  *   order, div  the activation row of place p is order[p] / div (the sort of
  *               sq_route with div = k), or p itself if order is NULL
  *   offsets     [E+1] i32, device, ascending from 0; the segments may be empty
- *   n           places: offsets[E] <= n, order has n entries, 1 <= n <= 2^24
+ *   n           places: offsets[E] <= n, order has n entries, 1 <= n <= 2^24 and
+ *               n * roundup(N,16) * roundup(K,128) < 2^51
  *   y           [n][N] f32 out; the rows from offsets[E] on are left as they were
  *   workspace   sq_grouped_linear_workspace_bytes bytes (may be 0), 16-byte
  *               aligned; scratch, it needs no zeroing.  Calls that may overlap
