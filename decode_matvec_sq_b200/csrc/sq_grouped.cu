@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
     first = incl - v;
     groups = __shfl_sync(0xffffffffu, incl, 31);
   } else {
-    groups = segment_units<kThreads>(a.offsets, a.E, a.n, a.status, TG, pre, part_i);
+    groups = segment_units(a.offsets, a.E, a.n, a.status, TG, pre, part_i);
   }
   // expert of group u, its first group and its places
   struct Group {

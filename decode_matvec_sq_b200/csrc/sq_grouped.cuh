@@ -76,9 +76,8 @@ __device__ __forceinline__ int source_row(const GroupedArgs& p, int at) {
 
 // Exclusive sums over the experts of ceil(segment / unit), into pre[0 .. E]
 // (shared memory; all threads of the CTA call it; part: one int per warp).
-template <int THREADS>
-__device__ int segment_units(const int32_t* offsets, int E, int n, int32_t* status, int unit, int* pre, int* part) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ inline int segment_units(const int32_t* offsets, int E, int n, int32_t* status, int unit, int* pre, int* part) {
+  const int THREADS = blockDim.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int carry = 0;
   for (int e0 = 0; e0 < E; e0 += THREADS) {
     const int e = e0 + (int)threadIdx.x;

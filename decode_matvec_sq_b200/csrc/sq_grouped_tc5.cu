@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ostart[g] = n_out;
   pdl_wait();
   pdl_launch_dependents();
-  const int units = segment_units<kThreads>(a.offsets, a.E, a.n, a.status, kTokens, pre, aux->part);
+  const int units = segment_units(a.offsets, a.E, a.n, a.status, kTokens, pre, aux->part);
   const int items = units * p.rt;
   fence_before();
   __syncthreads();

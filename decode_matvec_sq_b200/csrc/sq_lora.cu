@@ -44,7 +44,7 @@ namespace {
 constexpr int kCluster = 8;        // CTAs per cluster (the portable size)
 constexpr int kDecodeThreads = 256;
 constexpr int kGroup = 4;          // tokens per cluster of the decode kernel
-constexpr int kTile = 64;          // tokens per tile of the two-kernel route
+constexpr int kTile = 64;          // tokens per tile of the expand kernel
 constexpr int kExpandCols = 256;   // columns of y per piece of the decode expand
 
 struct Params {
@@ -66,6 +66,7 @@ struct Params {
   int Rp;     // R rounded up to 32
   int32_t* status;
   int pdl;
+  int cluster;  // shrink: CTAs per cluster
   int span;   // expand: columns per CTA
   int tiles;  // expand: CTAs along the tiles (the rest copy rows without adapter)
 };
@@ -282,6 +283,20 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// One k8 step on tf32 operands (the tensor cores read the upper 19 bits of each).
+__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// v = hi + lo: hi rounded to tf32's 11 bits, lo the exact rest.
+__device__ __forceinline__ void cut_tf32(float v, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(v));
+  lo = __float_as_uint(v - __uint_as_float(hi));
+}
+
 // Upper halves of two binary32 values as a pair of bfloat16 (first in the low half).
 __device__ __forceinline__ uint32_t upper_pair(float a, float b) {
   return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
@@ -312,54 +327,116 @@ struct Parts<__half> { static constexpr int n = 2; };
 template <>
 struct Parts<float> { static constexpr int n = 3; };
 
-// Elements i0 .. i0 + 7 of a weight row (`len` live) as bfloat16 parts.
-template <bool VEC, class W>
-__device__ __forceinline__ void weight_parts(const W* row, int i0, int len, uint32_t (&o)[Parts<W>::n][4]) {
-  if constexpr (std::is_same<W, __nv_bfloat16>::value && VEC) {
-    if (i0 + 8 <= len) {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(row + i0));
-      o[0][0] = a.x; o[0][1] = a.y; o[0][2] = a.z; o[0][3] = a.w;
-      return;
+// Eight neighbouring elements as they lie in memory, and their bfloat16 parts under
+// a mask (all ones or zero: what is masked may hold anything, NaN included).  The
+// loads of a step are issued together, without branches; a row without vector
+// alignment is gathered element by element instead.
+template <class T>
+struct Raw8 {
+  static constexpr int kWords = (int)sizeof(T) * 2;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
     }
   }
-  float v[8];
-  load_row8<VEC>(row, i0, len, v);
-  cut8<Parts<W>::n>(v, o);
+  // elements i0 .. i0 + 7 of a row of `len`, 0 past its end
+  __device__ __forceinline__ void gather(const T* row, int i0, int len) {
+    T v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i0 + i < len ? row[i0 + i] : T(0.0f);
+    __builtin_memcpy(w, v, sizeof(v));
+  }
+  // elements from n on become zero
+  __device__ __forceinline__ void keep(int n) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const int e = i * 4 / (int)sizeof(T);  // first element of the word
+      uint32_t m = e < n ? 0xffffffffu : 0u;
+      if (sizeof(T) == 2 && e + 1 >= n) m &= 0x0000ffffu;
+      w[i] &= m;
+    }
+  }
+  __device__ __forceinline__ void floats(float (&v)[8]) const {
+    if constexpr (std::is_same<T, float>::value) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    }
+  }
+  __device__ __forceinline__ void parts(uint32_t (&o)[Parts<T>::n][4]) const {
+    if constexpr (Parts<T>::n == 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[0][i] = w[i];
+    } else {
+      float v[8];
+      floats(v);
+      cut8<Parts<T>::n>(v, o);
+    }
+  }
+};
+// Elements i0 .. i0 + 7 of row `row` of a matrix of rows `ld` apart, `len` long; zero
+// unless `live`.  base points at a readable row in any case.
+template <bool VEC, class T>
+__device__ __forceinline__ void load_masked(Raw8<T>& r, const T* row, int i0, int len, bool live) {
+  if constexpr (VEC) {  // a vector lies inside the row or outside it, or crosses `len`
+    r.load(row + (i0 < len ? i0 : 0));
+    r.keep(live ? len - i0 : 0);
+  } else {
+    r.gather(row, i0, live ? len : 0);
+  }
 }
 
 // The MMA's k index is free as long as both operands agree: over 32 channels lane
 // tid4 holds channels 8 tid4 .. 8 tid4 + 7, the first four in one k16 step and the
 // last four in the next, so that every load is 16 bytes or more of a row.
-// Shrink: cluster = one tile of 64 tokens of one adapter; CTA c, warp half h take
-// slice 2c + h of the channels, warp pair (w % 4) the tokens 16 (w % 4) ...
-constexpr int kShrinkThreads = 256;
-constexpr int kSlices = 2 * kCluster;
+// Shrink: a cluster (of one CTA where there are tokens enough) takes 16 tokens of one
+// adapter, its warps split the channels; the parts meet in shared memory, then
+// over the cluster, and are summed in a fixed order.
+constexpr int kShrinkThreads = 512;
+constexpr int kGroupTokens = 16;
 
 template <class W, bool VEC, int NT>
 __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) {
-  extern __shared__ __align__(16) float sm[];  // [2 halves][kTile][Rp], then the tile sums [S + 1]
+  extern __shared__ __align__(16) float sm[];  // [warps][16][Rp], then the tile sums [S + 1]
   __shared__ int part_i[kShrinkThreads / 32];
   cg::cluster_group cluster = cg::this_cluster();
-  const int c = (int)cluster.block_rank(), u = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tid4 = lane & 3;
-  int* pre = reinterpret_cast<int*>(sm + 2 * kTile * p.Rp);
+  const int nc = p.cluster, c = (int)cluster.block_rank(), u = blockIdx.y;
+  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tid4 = lane & 3;
+  int* pre = reinterpret_cast<int*>(sm + warps * kGroupTokens * p.Rp);
   pdl_wait();
   pdl_launch_dependents();
-  const int units = segment_units<kShrinkThreads>(p.offsets, p.S, p.M, p.status, kTile, pre, part_i);
+  const int units = segment_units(p.offsets, p.S, p.M, p.status, kGroupTokens, pre, part_i);
   if (u >= units) return;  // (the whole cluster)
   const int a = unit_expert(pre, p.S, u);
   const int2 seg = segment_bounds(p.offsets, p.M, a, p.status);
-  const int p0 = seg.x + (u - pre[a]) * kTile, cnt = min(kTile, seg.y - p0);
+  const int p0 = seg.x + (u - pre[a]) * kGroupTokens, cnt = min(kGroupTokens, seg.y - p0);
   const int rank = adapter_rank(p, a);
-  const int tg = warp & 3, half = warp >> 2, first = 16 * tg;
-  const int steps = (p.K + 31) / 32, slice = 2 * c + half;
-  const int s0 = (int)((int64_t)steps * slice / kSlices), s1 = (int)((int64_t)steps * (slice + 1) / kSlices);
-  float* mine = sm + half * kTile * p.Rp;
-  if (first < cnt) {
+  const int steps = (p.K + 31) / 32, slice = c * warps + warp, slices = nc * warps;
+  const int s0 = (int)((int64_t)steps * slice / slices), s1 = (int)((int64_t)steps * (slice + 1) / slices);
+  float* mine = sm + warp * kGroupTokens * p.Rp;
+  {
     const float* xr[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      int t = __ldg(p.order + p0 + min(first + gid + 8 * h, cnt - 1));
+      int t = __ldg(p.order + p0 + min(gid + 8 * h, cnt - 1));
       if (t < 0 || t >= p.M) {
         set_status(p.status, SQ_ERR_INVALID_ARG);
         t = 0;
@@ -368,81 +445,127 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) 
     }
     const W* Aa = static_cast<const W*>(p.A) + (int64_t)a * p.R * p.K;
     for (int r0 = 0; r0 < p.Rp; r0 += 8 * NT) {  // (one pass up to rank 8 NT)
-      float acc[NT][4] = {};
+      // the products of leading parts, and the rest: an addition of the tensor cores
+      // may truncate, so the many small ones are kept from the large sum
+      constexpr bool SPLIT = Parts<W>::n > 1;
+      float acc[NT][4] = {}, low[SPLIT ? NT : 1][4] = {};
       if (r0 < rank) {
-#pragma unroll 2
         for (int s = s0; s < s1; ++s) {
           const int k = 32 * s + 8 * tid4;
-          uint32_t xa[2][3][4];
+          Raw8<float> xr8[2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float v[8];
-            load_row8<VEC>(xr[h], k, p.K, v);
-            cut8<3>(v, xa[h]);
-          }
+          for (int h = 0; h < 2; ++h) load_masked<VEC>(xr8[h], xr[h], k, p.K, true);
+          Raw8<W> wr8[NT];
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             const int r = r0 + 8 * j + gid;
-            if (r0 + 8 * j >= rank) break;
-            uint32_t w[Parts<W>::n][4];
-            weight_parts<VEC>(Aa + (int64_t)min(r, rank - 1) * p.K, k, r < rank ? p.K : 0, w);
+            load_masked<VEC>(wr8[j], Aa + (int64_t)min(r, rank - 1) * p.K, k, p.K, r < rank);
+          }
+          if constexpr (Parts<W>::n == 1) {
+            uint32_t xa[2][3][4];
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int h = 0; h < 2; ++h) xr8[h].parts(xa[h]);
 #pragma unroll
-              for (int i = 2; i >= 0; --i) {  // small products first
-                const uint32_t av[4] = {xa[0][i][2 * q], xa[1][i][2 * q], xa[0][i][2 * q + 1], xa[1][i][2 * q + 1]};
+            for (int j = 0; j < NT; ++j) {
+              if (r0 + 8 * j >= rank) break;
 #pragma unroll
-                for (int m = Parts<W>::n - 1; m >= 0; --m)
-                  if (i + m < 3) mma_bf16(acc[j], av, w[m][2 * q], w[m][2 * q + 1]);
+              for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 2; i >= 0; --i) {  // small products first
+                  const uint32_t av[4] = {xa[0][i][2 * q], xa[1][i][2 * q], xa[0][i][2 * q + 1], xa[1][i][2 * q + 1]};
+                  mma_bf16(acc[j], av, wr8[j].w[2 * q], wr8[j].w[2 * q + 1]);
+                }
+            }
+          } else {
+            // k8 step q: channels 2q, 2q + 1 of the lane's eight
+            uint32_t xh[2][8], xl[2][8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) cut_tf32(__uint_as_float(xr8[h].w[i]), xh[h][i], xl[h][i]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              if (r0 + 8 * j >= rank) break;
+              float wv[8];
+              wr8[j].floats(wv);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint32_t h0 = __float_as_uint(wv[2 * q]), h1 = __float_as_uint(wv[2 * q + 1]);
+                if constexpr (Parts<W>::n == 3) {
+                  uint32_t l0, l1;
+                  cut_tf32(wv[2 * q], h0, l0);
+                  cut_tf32(wv[2 * q + 1], h1, l1);
+                  mma_tf32(low[SPLIT ? j : 0], xh[0][2 * q], xh[1][2 * q], xh[0][2 * q + 1], xh[1][2 * q + 1], l0, l1);
+                }
+                mma_tf32(low[SPLIT ? j : 0], xl[0][2 * q], xl[1][2 * q], xl[0][2 * q + 1], xl[1][2 * q + 1], h0, h1);
+                mma_tf32(acc[j], xh[0][2 * q], xh[1][2 * q], xh[0][2 * q + 1], xh[1][2 * q + 1], h0, h1);
               }
+            }
           }
         }
+      }
+      if constexpr (SPLIT) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[j][i] += low[j][i];
       }
 #pragma unroll
       for (int j = 0; j < NT; ++j)
         if (r0 + 8 * j < p.Rp) {
-          float* o = mine + (first + gid) * p.Rp + r0 + 8 * j + 2 * tid4;
+          float* o = mine + gid * p.Rp + r0 + 8 * j + 2 * tid4;
           *reinterpret_cast<float2*>(o) = make_float2(acc[j][0], acc[j][1]);
           *reinterpret_cast<float2*>(o + 8 * p.Rp) = make_float2(acc[j][2], acc[j][3]);
         }
     }
   }
-  cluster.sync();
-  // CTA c sums its eighth of the tile's values over the slices, in order
-  const int total = cnt * p.Rp, i0 = (int)((int64_t)total * c / kCluster), i1 = (int)((int64_t)total * (c + 1) / kCluster);
+  __syncthreads();
+  // the CTA's parts summed into the first warp's, then the cluster's, CTA c taking
+  // its share of the values
+  const int total = cnt * p.Rp;
+  for (int i = threadIdx.x; i < total; i += blockDim.x) {
+    float v = sm[i];
+    for (int w = 1; w < warps; ++w) v += sm[w * kGroupTokens * p.Rp + i];
+    sm[i] = v;
+  }
+  if (nc > 1) cluster.sync();
+  else __syncthreads();
+  const int i0 = (int)((int64_t)total * c / nc), i1 = (int)((int64_t)total * (c + 1) / nc);
   const float sc = __ldg(p.scale + a);
   bool bad = false;
-  for (int i = i0 + threadIdx.x; i < i1; i += kShrinkThreads) {
+  for (int i = i0 + threadIdx.x; i < i1; i += blockDim.x) {
     float v = 0.0f;
-#pragma unroll
-    for (int d = 0; d < kCluster; ++d) {
-      const float* o = cluster.map_shared_rank(sm, d);
-      v += o[i] + o[kTile * p.Rp + i];
-    }
+    for (int d = 0; d < nc; ++d) v += nc > 1 ? cluster.map_shared_rank(sm, d)[i] : sm[i];
     bad |= !isfinite(v);
     p.v[(int64_t)p0 * p.Rp + i] = v * sc;
   }
   if (bad) set_status(p.status, SQ_ERR_NONFINITE);
-  cluster.sync();  // no CTA leaves while its parts may be read
+  if (nc > 1) cluster.sync();  // no CTA leaves while its parts may be read
 }
 
 constexpr int kExpandThreads = 128;
 constexpr int kBlockCols = 64;  // columns of y per warp pass
+constexpr int kRing = 4;        // units of the weight ring
 
-// Operands of v in the expand kernel: three bfloat16 parts, or two binary16 parts.
+// 16-byte words a lane holds of v per 32 of the rank in the expand kernel: three
+// bfloat16 parts for bfloat16 weights, two binary16 parts for binary16 ones; for
+// binary32 weights v itself, cut into tf32 parts when it is read.
 template <class W>
-constexpr int kVParts = std::is_same<W, __half>::value ? 2 : 3;
+constexpr int kVWords = std::is_same<W, __nv_bfloat16>::value ? 6 : 4;
 
 // Expand: CTA = one tile of 64 tokens (16 per warp) and a span of columns.  The
 // warp's v lies in shared memory in operand order ([k32 step][part][two 16-byte
 // words per lane]).  Of each 16 columns, one MMA takes columns 4i, 4i+1 and one
 // 4i+2, 4i+3 (i = 0..3), so that a lane's accumulators are four neighbouring
-// columns and base and y move in 16-byte words.
+// columns and base and y move in 16-byte words.  The next 64 columns of base are
+// copied into shared memory (each lane its own words) under the products of these.
 template <class W, bool VEC, bool VECY>
-__global__ void __launch_bounds__(kExpandThreads) k_lora_expand(const Params p) {
-  constexpr int NV = kVParts<W>;
-  constexpr bool HALF = NV == 2;
-  extern __shared__ __align__(16) uint4 vsm[];  // [4 warps][Rp / 32][NV][2][32], then the tile sums
+__global__ void __launch_bounds__(kExpandThreads, 4) k_lora_expand(const Params p) {
+  constexpr int NV = kVWords<W>;
+  constexpr bool BF = std::is_same<W, __nv_bfloat16>::value, HALF = std::is_same<W, __half>::value;
+  // [4 warps][Rp / 32][NV][32] of v, [4 warps][8][32] of base, the weight ring, the tile sums
+  extern __shared__ __align__(16) uint4 vsm[];
+  constexpr int kUnitWords = kBlockCols * 32 * (int)sizeof(W) / 16;  // 16-byte words of a ring unit
   __shared__ int part_i[kExpandThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tid4 = lane & 3;
   const int u = blockIdx.y;
@@ -459,21 +582,23 @@ __global__ void __launch_bounds__(kExpandThreads) k_lora_expand(const Params p) 
     return;
   }
   const int steps_all = p.Rp / 32;
-  int* pre = reinterpret_cast<int*>(vsm + 4 * steps_all * NV * 64);
-  const int units = segment_units<kExpandThreads>(p.offsets, p.S, p.M, p.status, kTile, pre, part_i);
+  uint4* ring = vsm + 4 * (steps_all * NV + 8) * 32;
+  int* pre = reinterpret_cast<int*>(ring + (VEC ? kRing * kUnitWords : 0));
+  const int units = segment_units(p.offsets, p.S, p.M, p.status, kTile, pre, part_i);
   if (u >= units) return;
   const int a = unit_expert(pre, p.S, u);
   const int2 seg = segment_bounds(p.offsets, p.M, a, p.status);
-  const int p0 = seg.x + (u - pre[a]) * kTile + 16 * warp, cnt = min(16, seg.y - p0);
-  if (cnt <= 0) return;  // (no barrier follows)
+  // (a warp without tokens repeats the tile's last: it helps copying the weights)
+  const int pt = seg.x + (u - pre[a]) * kTile, p0 = min(pt + 16 * warp, seg.y - 1), cnt = min(16, seg.y - (pt + 16 * warp));
   const int rank = adapter_rank(p, a), steps = (rank + 31) / 32;
-  uint4* vw = vsm + warp * steps_all * NV * 64;
+  uint4* vw = vsm + warp * steps_all * NV * 32;
+  uint4* bw = vsm + 4 * steps_all * NV * 32 + warp * 256 + lane;
   float back[2] = {1.0f, 1.0f};  // binary16 parts: 2^e of the two rows
   int64_t row[2];
   const float* vrow[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int at = p0 + min(gid + 8 * h, cnt - 1);
+    const int at = min(p0 + gid + 8 * h, seg.y - 1);
     int t = __ldg(p.order + at);
     if (t < 0 || t >= p.M) t = 0;  // (reported by the shrink kernel)
     row[h] = t;
@@ -503,111 +628,178 @@ __global__ void __launch_bounds__(kExpandThreads) k_lora_expand(const Params p) 
     }
   }
   for (int s = 0; s < steps; ++s) {
-    uint32_t o[2][3][4];
+    uint4* o4 = vw + s * NV * 32 + lane;
+    float v[2][8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[8];
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float4 f = *reinterpret_cast<const float4*>(vrow[h] + 32 * s + 8 * tid4 + 4 * i);
-        v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+        v[h][4 * i] = f.x; v[h][4 * i + 1] = f.y; v[h][4 * i + 2] = f.z; v[h][4 * i + 3] = f.w;
       }
-      if constexpr (HALF) {
+    if constexpr (BF || HALF) {
+      uint32_t o[2][3][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x0 = v[2 * i] * to[h], x1 = v[2 * i + 1] * to[h];
-          const __half2 hi = __floats2half2_rn(x0, x1);
-          const float2 hf = __half22float2(hi);
-          const __half2 lo = __floats2half2_rn(x0 - hf.x, x1 - hf.y);
-          o[h][0][i] = *reinterpret_cast<const uint32_t*>(&hi);
-          o[h][1][i] = *reinterpret_cast<const uint32_t*>(&lo);
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (HALF) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x0 = v[h][2 * i] * to[h], x1 = v[h][2 * i + 1] * to[h];
+            const __half2 hi = __floats2half2_rn(x0, x1);
+            const float2 hf = __half22float2(hi);
+            const __half2 lo = __floats2half2_rn(x0 - hf.x, x1 - hf.y);
+            o[h][0][i] = *reinterpret_cast<const uint32_t*>(&hi);
+            o[h][1][i] = *reinterpret_cast<const uint32_t*>(&lo);
+          }
+        } else {
+          cut8<3>(v[h], o[h]);
         }
-      } else {
-        cut8<3>(v, o[h]);
       }
+#pragma unroll
+      for (int i = 0; i < NV / 2; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          o4[(i * 2 + q) * 32] = make_uint4(o[0][i][2 * q], o[1][i][2 * q], o[0][i][2 * q + 1], o[1][i][2 * q + 1]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        o4[q * 32] = make_uint4(__float_as_uint(v[0][2 * q]), __float_as_uint(v[1][2 * q]), __float_as_uint(v[0][2 * q + 1]),
+                                __float_as_uint(v[1][2 * q + 1]));
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        vw[((s * NV + i) * 2 + q) * 32 + lane] =
-            make_uint4(o[0][i][2 * q], o[1][i][2 * q], o[0][i][2 * q + 1], o[1][i][2 * q + 1]);
   }
   __syncwarp();
   const W* Ba = static_cast<const W*>(p.B) + (int64_t)a * p.N * p.R;
   const int col = 4 * (gid >> 1) + (gid & 1);  // this lane's B column of each 16 (and + 2)
-  for (int c0 = n0; c0 < n1; c0 += kBlockCols) {
-    // base first: its latency passes under the products
-    float b[4][2][4];
+  const bool staged = VECY && p.base != nullptr;
+  // this lane's words of base of the 64 columns from c0
+  auto stage_base = [&](int c0) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int n = c0 + 16 * j + 4 * tid4;
-        const bool live = gid + 8 * h < cnt && p.base != nullptr;
-        if (VECY && live && n + 4 <= n1) {
-          const float4 f = *reinterpret_cast<const float4*>(p.base + row[h] * p.ldb + n);
-          b[j][h][0] = f.x; b[j][h][1] = f.y; b[j][h][2] = f.z; b[j][h][3] = f.w;
+        if (gid + 8 * h >= cnt || n >= n1) continue;
+        uint4* dst = bw + (j * 2 + h) * 32;
+        const float* src = p.base + row[h] * p.ldb + n;
+        if (n + 4 <= n1) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
         } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) b[j][h][i] = live && n + i < n1 ? p.base[row[h] * p.ldb + n + i] : 0.0f;
+          float* d = reinterpret_cast<float*>(dst);
+          for (int i = 0; n + i < n1; ++i) d[i] = src[i];
         }
       }
+  };
+  // ring unit i: 32 of the rank (step i % steps) of the 64 columns of block i / steps,
+  // column by column, copied by the whole CTA, kRing - 1 units ahead of its use
+  const int units_w = steps * ((n1 - n0 + kBlockCols - 1) / kBlockCols);
+  int next_c0 = n0, next_s = 0, issued = 0;
+  auto stage_weights = [&] {
+    if (VEC && issued < units_w) {
+      uint4* dst = ring + (issued % kRing) * kUnitWords;
+      constexpr int kWordElems = 16 / (int)sizeof(W), kRowWords = 32 / kWordElems;
+#pragma unroll
+      for (int i = 0; i < kUnitWords / kExpandThreads; ++i) {
+        const int w = threadIdx.x + i * kExpandThreads, n = w / kRowWords, e = 32 * next_s + (w % kRowWords) * kWordElems;
+        const W* src = Ba + (int64_t)min(next_c0 + n, n1 - 1) * p.R + (e < p.R ? e : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst + w)), "l"(src) : "memory");
+      }
+      if (++next_s == steps) {
+        next_s = 0;
+        next_c0 += kBlockCols;
+      }
+    }
+    ++issued;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int i = 0; i < kRing - 1; ++i) stage_weights();
+  int unit = 0;
+  for (int c0 = n0; c0 < n1; c0 += kBlockCols) {
+    if (staged) stage_base(c0);  // (with the next weight unit's group)
     float acc[8][4] = {};
     for (int s = 0; s < steps; ++s) {
-      uint32_t va[NV][2][4];
+      Raw8<W> wr8[8];
+      if constexpr (VEC) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+        __syncthreads();  // every thread's copies of this unit have landed, and the unit before is used
+        stage_weights();
+        const uint4* wu = ring + (unit % kRing) * kUnitWords;
+        ++unit;
+        constexpr int kLaneWords = (int)sizeof(W) / 2;  // 16-byte words of a lane's eight
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+        for (int j = 0; j < 8; ++j) {
+          const uint4* src = wu + (16 * (j >> 1) + col + 2 * (j & 1)) * 4 * kLaneWords + tid4 * kLaneWords;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint4 f = vw[((s * NV + i) * 2 + q) * 32 + lane];
-          va[i][q][0] = f.x; va[i][q][1] = f.y; va[i][q][2] = f.z; va[i][q][3] = f.w;
+          for (int i = 0; i < kLaneWords; ++i) {
+            const uint4 f = src[i];
+            wr8[j].w[4 * i] = f.x; wr8[j].w[4 * i + 1] = f.y; wr8[j].w[4 * i + 2] = f.z; wr8[j].w[4 * i + 3] = f.w;
+          }
+          if (32 * s + 32 > rank) wr8[j].keep(rank - 32 * s - 8 * tid4);
         }
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int n = c0 + 16 * (j >> 1) + col + 2 * (j & 1);
-        const W* wr = Ba + (int64_t)min(n, n1 - 1) * p.R;
-        if constexpr (HALF) {
-          uint32_t w[4];
-          if (VEC && 32 * s + 8 * tid4 + 8 <= rank) {
-            const uint4 f = __ldg(reinterpret_cast<const uint4*>(wr + 32 * s + 8 * tid4));
-            w[0] = f.x; w[1] = f.y; w[2] = f.z; w[3] = f.w;
-          } else {
+        for (int j = 0; j < 8; ++j) {
+          const int n = c0 + 16 * (j >> 1) + col + 2 * (j & 1);
+          wr8[j].gather(Ba + (int64_t)min(n, n1 - 1) * p.R, 32 * s + 8 * tid4, rank);
+        }
+      }
+      uint4 va[NV];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = 32 * s + 8 * tid4 + 2 * i;
-              const __half2 f = __halves2half2(r < rank ? wr[r] : __float2half(0.0f),
-                                               r + 1 < rank ? wr[r + 1] : __float2half(0.0f));
-              w[i] = *reinterpret_cast<const uint32_t*>(&f);
-            }
-          }
+      for (int i = 0; i < NV; ++i) va[i] = vw[(s * NV + i) * 32 + lane];
+      if constexpr (BF || HALF) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            mma_f16(acc[j], va[1][q], w[2 * q], w[2 * q + 1]);
-            mma_f16(acc[j], va[0][q], w[2 * q], w[2 * q + 1]);
-          }
-        } else {
-          uint32_t w[Parts<W>::n][4];
-          weight_parts<VEC>(wr, 32 * s + 8 * tid4, rank, w);
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
           for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int i = NV - 1; i >= 0; --i)
+            for (int i = NV / 2 - 1; i >= 0; --i) {  // small products first
+              const uint4 f = va[i * 2 + q];
+              const uint32_t av[4] = {f.x, f.y, f.z, f.w};
+              if constexpr (HALF) mma_f16(acc[j], av, wr8[j].w[2 * q], wr8[j].w[2 * q + 1]);
+              else mma_bf16(acc[j], av, wr8[j].w[2 * q], wr8[j].w[2 * q + 1]);
+            }
+      } else {
 #pragma unroll
-              for (int m = Parts<W>::n - 1; m >= 0; --m)
-                if (i + m < 3) mma_bf16(acc[j], va[i][q], w[m][2 * q], w[m][2 * q + 1]);
+        for (int q = 0; q < 4; ++q) {
+          uint32_t vh[4], vl[4];
+          cut_tf32(__uint_as_float(va[q].x), vh[0], vl[0]);
+          cut_tf32(__uint_as_float(va[q].y), vh[1], vl[1]);
+          cut_tf32(__uint_as_float(va[q].z), vh[2], vl[2]);
+          cut_tf32(__uint_as_float(va[q].w), vh[3], vl[3]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint32_t h0, h1, l0, l1;
+            cut_tf32(__uint_as_float(wr8[j].w[2 * q]), h0, l0);
+            cut_tf32(__uint_as_float(wr8[j].w[2 * q + 1]), h1, l1);
+            mma_tf32(acc[j], vh[0], vh[1], vh[2], vh[3], l0, l1);
+            mma_tf32(acc[j], vl[0], vl[1], vl[2], vl[3], h0, h1);
+            mma_tf32(acc[j], vh[0], vh[1], vh[2], vh[3], h0, h1);
+          }
         }
       }
+    }
+    // base went out with the group of this block's first unit: steps - 1 groups are newer
+    if (staged) {
+      if (!VEC || steps < 2) asm volatile("cp.async.wait_all;" ::: "memory");
+      else if (steps == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else asm volatile("cp.async.wait_group 2;" ::: "memory");
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (gid + 8 * h >= cnt) continue;
         const int n = c0 + 16 * j + 4 * tid4;
+        if (gid + 8 * h >= cnt || n >= n1) continue;
+        float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (staged) {
+          const float4 f = *reinterpret_cast<const float4*>(bw + (j * 2 + h) * 32);
+          b[0] = f.x; b[1] = f.y; b[2] = f.z; b[3] = f.w;
+        } else if (p.base) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) b[i] = n + i < n1 ? p.base[row[h] * p.ldb + n + i] : 0.0f;
+        }
         float o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = fmaf(acc[2 * j + (i >> 1)][2 * h + (i & 1)], back[h], b[j][h][i]);
+        for (int i = 0; i < 4; ++i) o[i] = fmaf(acc[2 * j + (i >> 1)][2 * h + (i & 1)], back[h], b[i]);
         float* yr = p.y + row[h] * p.ldy + n;
         if (VECY && n + 4 <= n1) {
           *reinterpret_cast<float4*>(yr) = make_float4(o[0], o[1], o[2], o[3]);
@@ -654,7 +846,7 @@ template <class W>
 cudaError_t launch_type(Params p, void* sort_ws, int32_t* sort_arrays, int sm_count, cudaStream_t stream) {
   // rows of A and x (B) start at addresses that allow 8-element vectors
   const bool veck = p.K % 8 == 0 && aligned(p.A, p.K, sizeof(W), 16) && aligned(p.x, p.K, 4, 16);
-  const bool vecr = aligned(p.B, p.R, sizeof(W), 16);
+  const bool vecr = p.R % 8 == 0 && aligned(p.B, p.R, sizeof(W), 16);
   const bool pdl = p.pdl != 0;
   if (p.M <= kLoraDecodeTokens) {
     const int ks = (int)ceil_div(ceil_div(p.K, 8), kCluster) * 8;
@@ -676,10 +868,16 @@ cudaError_t launch_type(Params p, void* sort_ws, int32_t* sort_arrays, int sm_co
   const int tiles = (int)(p.M / kTile + std::min(p.S, p.M));
   const int tables = (int)round_up(4 * (p.S + 1), 16);
   {
-    const int smem = 2 * kTile * p.Rp * 4 + tables;
+    // clusters only where 16 tokens a CTA leave SMs without work
+    const int64_t units = ceil_div(p.M, kGroupTokens);
+    p.cluster = 1;
+    while (p.cluster < kCluster && units * p.cluster * 2 <= sm_count) p.cluster *= 2;
+    const int threads = p.Rp <= 192 ? kShrinkThreads : kShrinkThreads / 2;  // (16 warps' parts must fit)
+    const int smem = threads / 32 * kGroupTokens * p.Rp * 4 + tables;
     auto* fn = p.Rp <= 32 ? (veck ? k_lora_shrink<W, true, 4> : k_lora_shrink<W, false, 4>)
                           : (veck ? k_lora_shrink<W, true, 8> : k_lora_shrink<W, false, 8>);
-    const cudaError_t e = launch(fn, dim3(kCluster, tiles), kShrinkThreads, smem, kCluster, true, stream, p);
+    const int groups = (int)(p.M / kGroupTokens + std::min(p.S, p.M));
+    const cudaError_t e = launch(fn, dim3(p.cluster, groups), threads, smem, p.cluster, true, stream, p);
     if (e != cudaSuccess) return e;
   }
   // columns per CTA: a few CTAs per SM over all tiles
@@ -688,7 +886,7 @@ cudaError_t launch_type(Params p, void* sort_ws, int32_t* sort_arrays, int sm_co
   p.tiles = tiles;
   const int copies = p.base == p.y ? 0 : (int)std::min<int64_t>(ceil_div(p.M, 64), 64);
   const bool vecy = aligned(p.y, p.ldy, 4, 16) && (!p.base || aligned(p.base, p.ldb, 4, 16));
-  const int smem = 4 * (p.Rp / 32) * kVParts<W> * 64 * 16 + tables;
+  const int smem = 4 * ((p.Rp / 32) * kVWords<W> + 8) * 32 * 16 + (vecr ? kRing * kBlockCols * 32 * (int)sizeof(W) : 0) + tables;
   auto* fn = vecr ? (vecy ? k_lora_expand<W, true, true> : k_lora_expand<W, true, false>)
                   : (vecy ? k_lora_expand<W, false, true> : k_lora_expand<W, false, false>);
   return launch(fn, dim3((unsigned)ceil_div(p.N, p.span), tiles + copies), kExpandThreads, smem, 1, true, stream, p);
