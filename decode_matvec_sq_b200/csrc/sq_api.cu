@@ -643,7 +643,7 @@ sq_status sq_route(const float* logits, int32_t T, int32_t E, int32_t k, int32_t
   sq_status st = check_device(&d);
   if (st != SQ_OK) return st;
   return from_cuda(launch_route(logits, T, E, k, gate == SQ_GATE_ALL, ids, gates, offsets, order, place, workspace,
-                                dev_status, (flags & SQ_LAUNCH_PDL) != 0, static_cast<cudaStream_t>(stream)));
+                                dev_status, static_cast<cudaStream_t>(stream)));
 }
 
 static bool segment_shape(int64_t n, int64_t S) { return n >= 1 && n <= kMaxEntries && S >= 1 && S <= kMaxSegments; }
@@ -666,7 +666,7 @@ sq_status sq_segment(const int32_t* ids, int32_t n, int32_t S, int32_t* offsets,
   sq_status st = check_device(&d);
   if (st != SQ_OK) return st;
   return from_cuda(launch_segment(ids, n, S, offsets, order, place, workspace, dev_status,
-                                  (flags & SQ_LAUNCH_PDL) != 0, static_cast<cudaStream_t>(stream)));
+                                  static_cast<cudaStream_t>(stream)));
 }
 
 // A stack of E experts of N rows in a layout the grouped kernels read.
@@ -762,7 +762,7 @@ sq_status sq_combine(const float* z, int32_t rows, const float* gates, const int
   DeviceInfo d;
   sq_status st = check_device(&d);
   if (st != SQ_OK) return st;
-  return from_cuda(launch_combine(z, rows, gates, place, T, k, N, base, out, dev_status, (flags & SQ_LAUNCH_PDL) != 0,
+  return from_cuda(launch_combine(z, rows, gates, place, T, k, N, base, out, dev_status,
                                   static_cast<cudaStream_t>(stream)));
 }
 
@@ -801,8 +801,8 @@ sq_status sq_lora_add(const sq_lora_bank* bank, const float* x, int32_t M, const
   if (need && (!workspace || ws_bytes < need)) return SQ_ERR_WORKSPACE;
   DeviceInfo d;
   if ((st = check_device(&d)) != SQ_OK) return st;
-  return from_cuda(launch_lora(*bank, x, M, ids, offsets, order, base, ld_base, y, ld_y, workspace, dev_status,
-                               (flags & SQ_LAUNCH_PDL) != 0, d.sm_count, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_lora(*bank, x, M, ids, offsets, order, base, ld_base, y, ld_y, workspace, dev_status, d.sm_count,
+                               static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -124,13 +124,13 @@ constexpr int kMaxChoices = 32;
 size_t segment_workspace_bytes(int64_t n, int S, int unit, bool route);
 cudaError_t launch_route(const float* logits, int T, int E, int k, bool all, int32_t* ids,
                          float* gates, int32_t* offsets, int32_t* order, int32_t* place,
-                         void* workspace, int32_t* status, bool pdl, cudaStream_t stream);
+                         void* workspace, int32_t* status, cudaStream_t stream);
 cudaError_t launch_segment(const int32_t* ids, int n, int S, int32_t* offsets, int32_t* order,
-                           int32_t* place, void* workspace, int32_t* status, bool pdl,
+                           int32_t* place, void* workspace, int32_t* status,
                            cudaStream_t stream);
 cudaError_t launch_combine(const float* z, int rows, const float* gates, const int32_t* place,
                            int T, int k, int N, const float* base, float* out, int32_t* status,
-                           bool pdl, cudaStream_t stream);
+                           cudaStream_t stream);
 
 // The expert-grouped linear layer (sq_grouped.cuh holds the arguments).
 struct GroupedArgs;
@@ -149,7 +149,7 @@ constexpr int kMaxLoraK = 65536;
 size_t lora_workspace_bytes(int M, int S, int R);
 cudaError_t launch_lora(const sq_lora_bank& bank, const float* x, int M, const int32_t* ids,
                         const int32_t* offsets, const int32_t* order, const float* base, int64_t ldb,
-                        float* y, int64_t ldy, void* workspace, int32_t* status, bool pdl,
-                        int sm_count, cudaStream_t stream);
+                        float* y, int64_t ldy, void* workspace, int32_t* status, int sm_count,
+                        cudaStream_t stream);
 
 }  // namespace sq

@@ -31,6 +31,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "sq_grouped.cuh"
@@ -42,10 +43,10 @@ namespace sq {
 namespace {
 
 constexpr int kCluster = 8;        // CTAs per cluster (the portable size)
+constexpr int kDecodeCluster = 16; // of the decode kernel
 constexpr int kDecodeThreads = 256;
-constexpr int kGroup = 4;          // tokens per cluster of the decode kernel
+constexpr int kGroup = 8;          // tokens per cluster of the decode kernel (MMA columns)
 constexpr int kTile = 64;          // tokens per tile of the expand kernel
-constexpr int kExpandCols = 256;   // columns of y per piece of the decode expand
 
 struct Params {
   const void* A;
@@ -65,8 +66,7 @@ struct Params {
   float* v;   // [M][Rp], in place order
   int Rp;     // R rounded up to 32
   int32_t* status;
-  int pdl;
-  int cluster;  // shrink: CTAs per cluster
+  int cluster;  // CTAs per cluster
   int span;   // expand: columns per CTA
   int tiles;  // expand: CTAs along the tiles (the rest copy rows without adapter)
 };
@@ -74,201 +74,6 @@ struct Params {
 __device__ __forceinline__ int adapter_rank(const Params& p, int a) {
   return p.rank ? min(max(__ldg(p.rank + a), 0), p.R) : p.R;
 }
-
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-// Eight consecutive elements from an address aligned to them.
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-
-// Elements i0 .. i0 + 7 of a row of `len` live elements (the rest 0, not read);
-// VEC: rows start at addresses that allow load8.
-template <bool VEC, class W>
-__device__ __forceinline__ void load_row8(const W* row, int i0, int len, float (&v)[8]) {
-  if (VEC && i0 + 8 <= len) {
-    load8(row + i0, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i0 + i < len ? to_f(row[i0 + i]) : 0.0f;
-  }
-}
-
-// ---- few tokens: one launch -------------------------------------------------------
-
-template <class W, bool VECK, bool VECR>
-__global__ void __launch_bounds__(kDecodeThreads) k_lora_decode(const Params p) {
-  extern __shared__ __align__(16) float sm[];
-  __shared__ int members[kGroup], n_members, adapter;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int c = (int)cluster.block_rank(), t = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kWarps = kDecodeThreads / 32;
-  if (p.pdl) {
-    pdl_wait();
-    pdl_launch_dependents();
-  }
-  // the tokens of t's adapter: this cluster serves t and the next of them if
-  // kGroup divides the number of them before t
-  if (warp == 0) {
-    const int a = __ldg(p.ids + t);
-    const bool ok = a >= 0 && a < p.S;
-    if (!ok && a != -1 && lane == 0) set_status(p.status, SQ_ERR_INVALID_ARG);
-    int before = 0, found = 0;
-    for (int u0 = 0; u0 < p.M; u0 += 32) {
-      const int u = u0 + lane;
-      const uint32_t same = __ballot_sync(0xffffffffu, ok && u < p.M && __ldg(p.ids + u) == a);
-      const uint32_t past = u0 > t ? 0xffffffffu : t - u0 >= 32 ? 0u : 0xffffffffu << (t - u0);
-      before += __popc(same & ~past);
-      const int at = found + __popc(same & past & ((1u << lane) - 1u));
-      if (((same & past) >> lane & 1u) && at < kGroup) members[at] = u;
-      found += __popc(same & past);
-    }
-    if (lane == 0) {
-      adapter = ok ? a : -1;
-      n_members = !ok ? 0 : before % kGroup == 0 ? min(found, kGroup) : -1;
-    }
-  }
-  __syncthreads();
-  const int nm = n_members, a = adapter;
-  const int n0 = (int)((int64_t)p.N * c / kCluster), n1 = (int)((int64_t)p.N * (c + 1) / kCluster);
-  if (nm <= 0) {  // no adapter (nm = 0: the base row as it is), or served by another cluster
-    if (nm == 0 && p.base != p.y)
-      for (int n = n0 + threadIdx.x; n < n1; n += kDecodeThreads)
-        p.y[t * p.ldy + n] = p.base ? p.base[t * p.ldb + n] : 0.0f;
-    return;  // (the whole cluster)
-  }
-  const int rank = adapter_rank(p, a);
-  // this CTA's channels, in units of 8
-  const int k8 = (p.K + 7) / 8;
-  const int k0 = (int)((int64_t)k8 * c / kCluster) * 8, k1 = min(p.K, (int)((int64_t)k8 * (c + 1) / kCluster) * 8);
-  const int ks = ((k8 + kCluster - 1) / kCluster) * 8;  // row stride of the x slice
-  float* xs = sm;                        // [kGroup][ks]
-  float* vp = xs + kGroup * ks;          // [kGroup][R]: this CTA's part of v
-  float* vs = vp + kGroup * p.R;         // [kGroup][R rounded up to 8]: v
-  const int Rv = (p.R + 7) & ~7;
-  float* out = vs + kGroup * Rv;         // [kGroup][kExpandCols]
-  for (int i = threadIdx.x; i < kGroup * ks; i += kDecodeThreads) {
-    const int g = i / ks, k = k0 + i % ks;
-    xs[i] = g < nm && k < k1 ? __ldg(p.x + (int64_t)members[g] * p.K + k) : 0.0f;
-  }
-  __syncthreads();
-  const W* Aa = static_cast<const W*>(p.A) + (int64_t)a * p.R * p.K + k0;
-  const int len = max(0, k1 - k0);
-  for (int r0 = warp * 4; r0 < rank; r0 += kWarps * 4) {
-    float acc[4][kGroup] = {};
-    for (int i0 = lane * 8; i0 < len; i0 += 256) {
-      float w[4][8];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const bool live = r0 + r < rank;
-        load_row8<VECK>(Aa + (int64_t)(live ? r0 + r : r0) * p.K, i0, live ? len : 0, w[r]);
-      }
-#pragma unroll
-      for (int g = 0; g < kGroup; ++g) {
-        const float4 x0 = *reinterpret_cast<const float4*>(xs + g * ks + i0);
-        const float4 x1 = *reinterpret_cast<const float4*>(xs + g * ks + i0 + 4);
-        const float xv[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[r][g] = fmaf(w[r][i], xv[i], acc[r][g]);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int g = 0; g < kGroup; ++g) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) acc[r][g] += __shfl_xor_sync(0xffffffffu, acc[r][g], o);
-        if (lane == 0 && r0 + r < rank) vp[g * p.R + r0 + r] = acc[r][g];
-      }
-  }
-  cluster.sync();
-  bool bad = false;
-  const float sc = __ldg(p.scale + a);
-  for (int i = threadIdx.x; i < kGroup * Rv; i += kDecodeThreads) {
-    const int g = i / Rv, r = i % Rv;
-    float v = 0.0f;
-    if (g < nm && r < rank) {
-#pragma unroll
-      for (int d = 0; d < kCluster; ++d) v += *cluster.map_shared_rank(vp + g * p.R + r, d);
-      bad |= !isfinite(v);
-      v *= sc;
-    }
-    vs[i] = v;
-  }
-  if (bad) set_status(p.status, SQ_ERR_NONFINITE);
-  // the parts have been read: no CTA leaves before every other has got here
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  __syncthreads();
-  const W* Ba = static_cast<const W*>(p.B) + (int64_t)a * p.N * p.R;
-  const int nv = (rank + 7) / 8;                       // vectors of 8 per row of B
-  int lpr = 1;                                         // lanes per row: a power of two <= nv
-  while (lpr * 2 <= nv && lpr < 32) lpr *= 2;
-  const int sub = lane & (lpr - 1), rpw = 32 / lpr;    // rows per warp pass
-  for (int c0 = n0; c0 < n1; c0 += kExpandCols) {
-    const int cols = min(kExpandCols, n1 - c0);
-    // (every lane of a warp takes the same number of passes)
-    for (int b0 = warp * rpw; b0 < cols; b0 += kWarps * rpw) {
-      const int n = b0 + lane / lpr;
-      float acc[kGroup] = {};
-      for (int j = sub; j < nv; j += lpr) {
-        float w[8];
-        load_row8<VECR>(Ba + (int64_t)(c0 + min(n, cols - 1)) * p.R, 8 * j, rank, w);
-#pragma unroll
-        for (int g = 0; g < kGroup; ++g) {
-          const float4 x0 = *reinterpret_cast<const float4*>(vs + g * Rv + 8 * j);
-          const float4 x1 = *reinterpret_cast<const float4*>(vs + g * Rv + 8 * j + 4);
-          const float xv[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[g] = fmaf(w[i], xv[i], acc[g]);
-        }
-      }
-#pragma unroll
-      for (int g = 0; g < kGroup; ++g) {
-        for (int o = lpr >> 1; o > 0; o >>= 1) acc[g] += __shfl_xor_sync(0xffffffffu, acc[g], o);
-        if (sub == 0 && n < cols) out[g * kExpandCols + n] = acc[g];
-      }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < nm * kExpandCols; i += kDecodeThreads) {
-      const int g = i / kExpandCols, n = i % kExpandCols;
-      if (n < cols) {
-        const int64_t row = members[g];
-        const float b = p.base ? p.base[row * p.ldb + c0 + n] : 0.0f;
-        p.y[row * p.ldy + c0 + n] = b + out[i];
-      }
-    }
-    __syncthreads();
-  }
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-
-// ---- many tokens: tensor cores ---------------------------------------------------------
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -407,6 +212,257 @@ __device__ __forceinline__ void load_masked(Raw8<T>& r, const T* row, int i0, in
 // The MMA's k index is free as long as both operands agree: over 32 channels lane
 // tid4 holds channels 8 tid4 .. 8 tid4 + 7, the first four in one k16 step and the
 // last four in the next, so that every load is 16 bytes or more of a row.
+// ---- few tokens: one launch -------------------------------------------------------
+// Weights are the MMA's rows (16 of A's rank, or 16 columns of y), the group's
+// tokens its eight columns.  A lane holds the activations (then v) of token gid.
+// Each weight word is loaded once, from memory straight into operand registers.
+
+// acc (+ low) += A x over one 32-channel step: rows w0 (gid) and w1 (gid + 8), columns'
+// operand parts x.
+template <class W>
+struct Columns;
+template <>
+struct Columns<__nv_bfloat16> {
+  uint32_t p[3][4];
+  __device__ __forceinline__ void set(float (&v)[8]) { cut8<3>(v, p); }
+  __device__ __forceinline__ void mma(float (&acc)[4], float (&)[4], const Raw8<__nv_bfloat16>& w0,
+                                      const Raw8<__nv_bfloat16>& w1) const {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t a[4] = {w0.w[2 * q], w1.w[2 * q], w0.w[2 * q + 1], w1.w[2 * q + 1]};
+#pragma unroll
+      for (int i = 2; i >= 0; --i) mma_bf16(acc, a, p[i][2 * q], p[i][2 * q + 1]);
+    }
+  }
+};
+template <class W>
+struct Columns32 {  // tf32 parts
+  uint32_t h[8], l[8];
+  __device__ __forceinline__ void set(float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cut_tf32(v[i], h[i], l[i]);
+  }
+  __device__ __forceinline__ void mma(float (&acc)[4], float (&low)[4], const Raw8<W>& w0, const Raw8<W>& w1) const {
+    float f0[8], f1[8];
+    w0.floats(f0);
+    w1.floats(f1);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t a[4] = {__float_as_uint(f0[2 * q]), __float_as_uint(f1[2 * q]), __float_as_uint(f0[2 * q + 1]),
+                       __float_as_uint(f1[2 * q + 1])};
+      if constexpr (Parts<W>::n == 3) {
+        uint32_t b[4];
+        cut_tf32(f0[2 * q], a[0], b[0]);
+        cut_tf32(f1[2 * q], a[1], b[1]);
+        cut_tf32(f0[2 * q + 1], a[2], b[2]);
+        cut_tf32(f1[2 * q + 1], a[3], b[3]);
+        mma_tf32(low, b[0], b[1], b[2], b[3], h[2 * q], h[2 * q + 1]);
+      }
+      mma_tf32(low, a[0], a[1], a[2], a[3], l[2 * q], l[2 * q + 1]);
+      mma_tf32(acc, a[0], a[1], a[2], a[3], h[2 * q], h[2 * q + 1]);
+    }
+  }
+};
+template <>
+struct Columns<__half> : Columns32<__half> {};
+template <>
+struct Columns<float> : Columns32<float> {};
+
+template <class W, bool VECK, bool VECR>
+__global__ void __launch_bounds__(kDecodeThreads, 2) k_lora_decode(const Params p) {
+  extern __shared__ __align__(16) float sm[];
+  __shared__ int members[kGroup], n_members, adapter;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int nc = p.cluster, c = (int)cluster.block_rank(), u = blockIdx.y;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tid4 = lane & 3;
+  constexpr int kWarps = kDecodeThreads / 32;
+  pdl_wait();
+  pdl_launch_dependents();
+  // Tokens that share an adapter form groups of up to kGroup, in token order; cluster
+  // u takes the u-th group, the clusters behind the groups one token without an
+  // adapter each, and the rest of the grid has nothing to do (it comes last, so it
+  // keeps no SM from a group).
+  if (warp == 0) {
+    static_assert(kLoraDecodeTokens == 64, "two tokens a lane");
+    int id[2], before[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = lane + 32 * h;
+      const int a = k < p.M ? __ldg(p.ids + k) : -2;
+      id[h] = a >= 0 && a < p.S ? a : k < p.M ? -1 : -2;
+      if (k < p.M && id[h] < 0 && a != -1) set_status(p.status, SQ_ERR_INVALID_ARG);
+      before[h] = __popc(__match_any_sync(0xffffffffu, id[h]) & ((1u << lane) - 1u));
+    }
+    for (int i = 0; i < 32; ++i) before[1] += __shfl_sync(0xffffffffu, id[0], i) == id[1];
+    uint32_t lead[2], none[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      lead[h] = __ballot_sync(0xffffffffu, id[h] >= 0 && before[h] % kGroup == 0);
+      none[h] = __ballot_sync(0xffffffffu, id[h] == -1);
+    }
+    const int groups = __popc(lead[0]) + __popc(lead[1]);
+    int want = u, a = -1, n = -1, first = 0;  // the want-th set bit of lead (or none)
+    const uint32_t* bits = u < groups ? lead : none;
+    if (u >= groups) want -= groups;
+    const int half = want >= __popc(bits[0]) ? 1 : 0;
+    if (half) want -= __popc(bits[0]);
+    const uint32_t word = bits[half];
+    const bool mine = (word >> lane & 1u) && __popc(word & ((1u << lane) - 1u)) == want;
+    const uint32_t at = __ballot_sync(0xffffffffu, mine);
+    if (at) {
+      const int src = __ffs(at) - 1;
+      a = __shfl_sync(0xffffffffu, half ? id[1] : id[0], src);
+      first = __shfl_sync(0xffffffffu, half ? before[1] : before[0], src);
+      n = 0;
+      if (a < 0 && lane == 0) members[0] = src + 32 * half;
+    }
+    if (a >= 0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool in = id[h] == a && before[h] >= first && before[h] < first + kGroup;
+        if (in) members[before[h] - first] = lane + 32 * h;
+        n += __popc(__ballot_sync(0xffffffffu, in));
+      }
+    }
+    if (lane == 0) {
+      adapter = a;
+      n_members = n;  // 0: a token without an adapter; -1: nothing to do
+    }
+  }
+  __syncthreads();
+  const int nm = n_members, a = adapter;
+  // this CTA's columns, in blocks of 16
+  const int nb = (p.N + 15) / 16;
+  const int n0 = nb * c / nc * 16, n1 = min(p.N, nb * (c + 1) / nc * 16);
+  if (nm <= 0) {
+    const int64_t t = members[0];  // no adapter: the base row as it is
+    if (nm == 0 && p.base != p.y)
+      for (int n = n0 + threadIdx.x; n < n1; n += kDecodeThreads)
+        p.y[t * p.ldy + n] = p.base ? p.base[t * p.ldb + n] : 0.0f;
+    return;  // (the whole cluster)
+  }
+  const int rank = adapter_rank(p, a), R16 = (p.R + 15) & ~15;
+  const W* Ba = static_cast<const W*>(p.B) + (int64_t)a * p.N * p.R;
+  float* part = sm;                             // [kWarps][R16][8]: v of each warp, then [R16][8] of the CTA
+  float* vs = part + kWarps * R16 * 8;          // [R16 rounded up to 32][8]: v
+  // ---- v = A x: warp slices of the channels, 32 at a time
+  {
+    const float* xrow = p.x + (int64_t)members[min(gid, nm - 1)] * p.K;
+    const W* Aa = static_cast<const W*>(p.A) + (int64_t)a * p.R * p.K;
+    const int steps = (p.K + 31) / 32, slice = c * kWarps + warp, slices = nc * kWarps;
+    const int s0 = (int)((int64_t)steps * slice / slices), s1 = (int)((int64_t)steps * (slice + 1) / slices);
+    for (int r0 = 0; r0 < rank; r0 += 64) {
+      float acc[4][4] = {}, low[4][4] = {};
+      for (int s = s0; s < s1; ++s) {
+        const int k = 32 * s + 8 * tid4;
+        Raw8<float> xr;
+        load_masked<VECK>(xr, xrow, k, p.K, true);
+        Raw8<W> w[4][2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = r0 + 16 * j + gid + 8 * h;
+            if (r0 + 16 * j < rank) load_masked<VECK>(w[j][h], Aa + (int64_t)min(r, rank - 1) * p.K, k, p.K, r < rank);
+          }
+        float xf[8];
+        xr.floats(xf);
+        Columns<W> x;
+        x.set(xf);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (r0 + 16 * j < rank) x.mma(acc[j], low[j], w[j][0], w[j][1]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (r0 + 16 * j < rank) {
+          float* o = part + (warp * R16 + r0 + 16 * j + gid) * 8 + 2 * tid4;
+          *reinterpret_cast<float2*>(o) = make_float2(acc[j][0] + low[j][0], acc[j][1] + low[j][1]);
+          *reinterpret_cast<float2*>(o + 64) = make_float2(acc[j][2] + low[j][2], acc[j][3] + low[j][3]);
+        }
+    }
+  }
+  __syncthreads();
+  const int live = (rank + 15) / 16 * 16 * 8;  // values computed
+  for (int i = threadIdx.x; i < live; i += kDecodeThreads) {
+    float v = part[i];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) v += part[w * R16 * 8 + i];
+    part[i] = v;
+  }
+  cluster.sync();
+  bool bad = false;
+  const float sc = __ldg(p.scale + a);
+  const int steps = (rank + 31) / 32;
+  for (int i = threadIdx.x; i < steps * 32 * 8; i += kDecodeThreads) {
+    float v = 0.0f;
+    if (i < live) {
+#pragma unroll 8
+      for (int d = 0; d < nc; ++d) v += cluster.map_shared_rank(part, d)[i];
+      bad |= (i & 7) < nm && !isfinite(v);
+      v *= sc;
+    }
+    vs[i] = v;
+  }
+  if (bad) set_status(p.status, SQ_ERR_NONFINITE);
+  // the parts have been read: no CTA leaves before every other has got here
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  __syncthreads();
+  // ---- y += B v: 16 columns at a time, two blocks' weights in flight
+  const float* by[2];
+  float* yy[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {  // the accumulators' tokens
+    const int64_t row = members[min(2 * tid4 + i, nm - 1)];
+    by[i] = p.base ? p.base + row * p.ldb : nullptr;
+    yy[i] = p.y + row * p.ldy;
+  }
+  constexpr int kAhead = 2;
+  for (int b0 = n0 + 16 * kAhead * warp; b0 < n1; b0 += 16 * kAhead * kWarps) {
+    float b[kAhead][4], acc[kAhead][4] = {}, low[kAhead][4] = {};
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = b0 + 16 * u + gid + 8 * (i >> 1);
+        b[u][i] = by[i & 1] && n < n1 && 2 * tid4 + (i & 1) < nm ? by[i & 1][n] : 0.0f;
+      }
+    constexpr int kSteps = sizeof(W) == 2 ? 2 : 1;  // steps of the rank loaded together
+    for (int s0 = 0; s0 < steps; s0 += kSteps) {
+      Raw8<W> w[kSteps][kAhead][2];
+#pragma unroll
+      for (int e = 0; e < kSteps; ++e)
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            load_masked<VECR>(w[e][u][h], Ba + (int64_t)min(b0 + 16 * u + gid + 8 * h, n1 - 1) * p.R,
+                              32 * (s0 + e) + 8 * tid4, rank, true);
+#pragma unroll
+      for (int e = 0; e < kSteps; ++e) {
+        if (s0 + e >= steps) break;
+        float vf[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) vf[i] = vs[(32 * (s0 + e) + 8 * tid4 + i) * 8 + gid];
+        Columns<W> v;
+        v.set(vf);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) v.mma(acc[u], low[u], w[e][u][0], w[e][u][1]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = b0 + 16 * u + gid + 8 * (i >> 1);
+        if (n < n1 && 2 * tid4 + (i & 1) < nm) yy[i & 1][n] = b[u][i] + (acc[u][i] + low[u][i]);
+      }
+  }
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// ---- many tokens ------------------------------------------------------------------------
 // Shrink: a cluster (of one CTA where there are tokens enough) takes 16 tokens of one
 // adapter, its warps split the channels; the parts meet in shared memory, then
 // over the cluster, and are summed in a fixed order.
@@ -847,19 +903,32 @@ cudaError_t launch_type(Params p, void* sort_ws, int32_t* sort_arrays, int sm_co
   // rows of A and x (B) start at addresses that allow 8-element vectors
   const bool veck = p.K % 8 == 0 && aligned(p.A, p.K, sizeof(W), 16) && aligned(p.x, p.K, 4, 16);
   const bool vecr = p.R % 8 == 0 && aligned(p.B, p.R, sizeof(W), 16);
-  const bool pdl = p.pdl != 0;
   if (p.M <= kLoraDecodeTokens) {
-    const int ks = (int)ceil_div(ceil_div(p.K, 8), kCluster) * 8;
-    const int smem = 4 * kGroup * (ks + p.R + (int)round_up(p.R, 8) + kExpandCols) + 16;
+    const int R16 = (int)round_up(p.R, 16);
+    const int smem = 4 * 8 * (kDecodeThreads / 32 * R16 + (int)round_up(p.R, 32));
+    // 16 CTAs a cluster for few tokens (5.8 against 6.6 us for one), but only some 16
+    // such clusters run at a time (64 tokens over 32 adapters: 37 against 27 us)
+    p.cluster = p.M <= 16 ? kDecodeCluster : kCluster;
     auto* fn = veck ? (vecr ? k_lora_decode<W, true, true> : k_lora_decode<W, true, false>)
                     : (vecr ? k_lora_decode<W, false, true> : k_lora_decode<W, false, false>);
-    return launch(fn, dim3(kCluster, p.M), kDecodeThreads, smem, kCluster, pdl, stream, p);
+    // clusters above the portable size: allowed once per kernel and device
+    static std::atomic<uint64_t> allowed[4];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::atomic<uint64_t>& mask = allowed[(veck ? 2 : 0) + (vecr ? 1 : 0)];
+    if (p.cluster > kCluster && !(mask.load() >> dev & 1u)) {
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      mask.fetch_or(1ull << dev);
+    }
+    return launch(fn, dim3(p.cluster, p.M), kDecodeThreads, smem, p.cluster, true, stream, p);
   }
   if (!p.offsets) {
     int32_t* offsets = sort_arrays;
     int32_t* order = offsets + round_up(p.S + 1, 4);
     int32_t* place = order + round_up(p.M, 4);
-    const cudaError_t e = launch_segment(p.ids, p.M, p.S, offsets, order, place, sort_ws, p.status, pdl, stream);
+    const cudaError_t e = launch_segment(p.ids, p.M, p.S, offsets, order, place, sort_ws, p.status, stream);
     if (e != cudaSuccess) return e;
     p.offsets = offsets;
     p.order = order;
@@ -916,7 +985,7 @@ size_t lora_workspace_bytes(int M, int S, int R) { return M <= kLoraDecodeTokens
 
 cudaError_t launch_lora(const sq_lora_bank& bank, const float* x, int M, const int32_t* ids, const int32_t* offsets,
                         const int32_t* order, const float* base, int64_t ldb, float* y, int64_t ldy, void* workspace,
-                        int32_t* status, bool pdl, int sm_count, cudaStream_t stream) {
+                        int32_t* status, int sm_count, cudaStream_t stream) {
   Params p = {};
   p.A = bank.A;
   p.B = bank.B;
@@ -937,7 +1006,6 @@ cudaError_t launch_lora(const sq_lora_bank& bank, const float* x, int M, const i
   p.order = order;
   p.Rp = (int)round_up(bank.R, 32);
   p.status = status;
-  p.pdl = pdl ? 1 : 0;
   void* sort_ws = nullptr;
   int32_t* arrays = nullptr;
   if (M > kLoraDecodeTokens) {

@@ -256,25 +256,21 @@ __device__ void finish_single(const SegSmem& sm, const SegParams& p) {
 }
 
 template <int I>
-__global__ void __launch_bounds__(kThreads, 1) k_route_one(const RouteParams r, const SegParams p, int pdl) {
+__global__ void __launch_bounds__(kThreads, 1) k_route_one(const RouteParams r, const SegParams p) {
   extern __shared__ int smem[];
   const SegSmem sm(smem, p.chunk, p.S);
-  if (pdl) {
-    pdl_wait();
-    pdl_launch_dependents();
-  }
+  pdl_wait();
+  pdl_launch_dependents();
   route_tokens<I>(r, sm, 0, r.T);
   __syncthreads();
   finish_single(sm, p);
 }
 
-__global__ void __launch_bounds__(kThreads, 1) k_segment_one(const SegParams p, int pdl) {
+__global__ void __launch_bounds__(kThreads, 1) k_segment_one(const SegParams p) {
   extern __shared__ int smem[];
   const SegSmem sm(smem, p.chunk, p.S);
-  if (pdl) {
-    pdl_wait();
-    pdl_launch_dependents();
-  }
+  pdl_wait();
+  pdl_launch_dependents();
   load_ids(sm, p, 0, p.n);
   __syncthreads();
   finish_single(sm, p);
@@ -283,13 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_segment_one(const SegParams p, 
 // First launch over many entries: (route the chunk's tokens,) count its
 // entries per segment.
 template <int I>
-__global__ void __launch_bounds__(kThreads, 1) k_count(const RouteParams r, const SegParams p, int pdl) {
+__global__ void __launch_bounds__(kThreads, 1) k_count(const RouteParams r, const SegParams p) {
   extern __shared__ int smem[];
   const SegSmem sm(smem, p.chunk, p.S);
-  if (pdl) {
-    pdl_wait();
-    pdl_launch_dependents();
-  }
+  pdl_wait();
   const int e0 = blockIdx.x * p.chunk, n = min(p.chunk, p.n - e0);
   for (int i = threadIdx.x; i < p.S; i += kThreads) sm.total[i] = 0;
   if constexpr (I > 0) {
@@ -306,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_count(const RouteParams r, cons
   }
   __syncthreads();
   for (int s = threadIdx.x; s < p.S; s += kThreads) p.counts[(int64_t)blockIdx.x * p.S + s] = sm.total[s];
+  pdl_launch_dependents();
 }
 
 // Second launch: every CTA sums the chunks' counts and places its own entries.
@@ -353,11 +347,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_place(const SegParams p) {
 template <bool VEC>
 __global__ void __launch_bounds__(256) k_combine(const float* __restrict__ z, int rows, const float* __restrict__ gates,
                                                  const int32_t* __restrict__ place, int k, int N,
-                                                 const float* base, float* out, int32_t* status, int pdl) {
-  if (pdl) {
-    pdl_wait();
-    pdl_launch_dependents();
-  }
+                                                 const float* base, float* out, int32_t* status) {
+  pdl_wait();
+  pdl_launch_dependents();
   const int t = blockIdx.x;
   const int c = (blockIdx.y * 256 + threadIdx.x) * (VEC ? 4 : 1);
   if (c >= N) return;
@@ -403,8 +395,10 @@ __global__ void __launch_bounds__(256) k_combine(const float* __restrict__ z, in
   }
 }
 
+// Every kernel here begins by waiting for the one before it, so its launch may always
+// be brought forward (programmatic dependent launch).
 template <class... Args>
-cudaError_t launch(void (*fn)(Args...), dim3 grid, int threads, int smem, bool pdl, cudaStream_t stream, Args... args) {
+cudaError_t launch(void (*fn)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream, Args... args) {
   if (smem > 48 * 1024) {
     const cudaError_t e = ensure_smem_attr((const void*)fn, smem);
     if (e != cudaSuccess) return e;
@@ -418,7 +412,7 @@ cudaError_t launch(void (*fn)(Args...), dim3 grid, int threads, int smem, bool p
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
@@ -448,47 +442,47 @@ size_t segment_workspace_bytes(int64_t n, int S, int unit, bool route) {
 }
 
 cudaError_t launch_route(const float* logits, int T, int E, int k, bool all, int32_t* ids, float* gates,
-                         int32_t* offsets, int32_t* order, int32_t* place, void* workspace, int32_t* status, bool pdl,
+                         int32_t* offsets, int32_t* order, int32_t* place, void* workspace, int32_t* status,
                          cudaStream_t stream) {
   RouteParams r{logits, T, E, k, all ? 1 : 0, ids, gates, status};
   SegParams p{ids, T * k, E, T * k, 1, offsets, order, place, static_cast<int32_t*>(workspace), status};
   if (segment_workspace_bytes(p.n, E, k, true) == 0) {
     const int smem = 4 * seg_smem_ints(p.chunk, E);
     return with_lanes(E, [&](auto I) {
-      return launch(k_route_one<decltype(I)::value>, dim3(1), kThreads, smem, pdl, stream, r, p, pdl ? 1 : 0);
+      return launch(k_route_one<decltype(I)::value>, dim3(1), kThreads, smem, stream, r, p);
     });
   }
   p.chunk = chunk_entries(p.n, k);
   p.chunks = (int)ceil_div(p.n, p.chunk);
   const int smem = 4 * seg_smem_ints(p.chunk, E);
   const cudaError_t e = with_lanes(E, [&](auto I) {
-    return launch(k_count<decltype(I)::value>, dim3(p.chunks), kThreads, smem, pdl, stream, r, p, pdl ? 1 : 0);
+    return launch(k_count<decltype(I)::value>, dim3(p.chunks), kThreads, smem, stream, r, p);
   });
   if (e != cudaSuccess) return e;
-  return launch(k_place, dim3(p.chunks), kThreads, smem, true, stream, p);
+  return launch(k_place, dim3(p.chunks), kThreads, smem, stream, p);
 }
 
 cudaError_t launch_segment(const int32_t* ids, int n, int S, int32_t* offsets, int32_t* order, int32_t* place,
-                           void* workspace, int32_t* status, bool pdl, cudaStream_t stream) {
+                           void* workspace, int32_t* status, cudaStream_t stream) {
   SegParams p{ids, n, S, n, 1, offsets, order, place, static_cast<int32_t*>(workspace), status};
   if (segment_workspace_bytes(n, S, 1, false) == 0)
-    return launch(k_segment_one, dim3(1), kThreads, 4 * seg_smem_ints(n, S), pdl, stream, p, pdl ? 1 : 0);
+    return launch(k_segment_one, dim3(1), kThreads, 4 * seg_smem_ints(n, S), stream, p);
   p.chunk = chunk_entries(n, 1);
   p.chunks = (int)ceil_div(n, p.chunk);
   const int smem = 4 * seg_smem_ints(p.chunk, S);
   const cudaError_t e =
-      launch(k_count<0>, dim3(p.chunks), kThreads, smem, pdl, stream, RouteParams{}, p, pdl ? 1 : 0);
+      launch(k_count<0>, dim3(p.chunks), kThreads, smem, stream, RouteParams{}, p);
   if (e != cudaSuccess) return e;
-  return launch(k_place, dim3(p.chunks), kThreads, smem, true, stream, p);
+  return launch(k_place, dim3(p.chunks), kThreads, smem, stream, p);
 }
 
 cudaError_t launch_combine(const float* z, int rows, const float* gates, const int32_t* place, int T, int k, int N,
-                           const float* base, float* out, int32_t* status, bool pdl, cudaStream_t stream) {
+                           const float* base, float* out, int32_t* status, cudaStream_t stream) {
   if ((N & 3) == 0)
-    return launch(k_combine<true>, dim3(T, (unsigned)ceil_div(N, 1024)), 256, 0, pdl, stream, z, rows, gates, place, k,
-                  N, base, out, status, pdl ? 1 : 0);
-  return launch(k_combine<false>, dim3(T, (unsigned)ceil_div(N, 256)), 256, 0, pdl, stream, z, rows, gates, place, k, N,
-                base, out, status, pdl ? 1 : 0);
+    return launch(k_combine<true>, dim3(T, (unsigned)ceil_div(N, 1024)), 256, 0, stream, z, rows, gates, place, k,
+                  N, base, out, status);
+  return launch(k_combine<false>, dim3(T, (unsigned)ceil_div(N, 256)), 256, 0, stream, z, rows, gates, place, k, N,
+                base, out, status);
 }
 
 }  // namespace sq
