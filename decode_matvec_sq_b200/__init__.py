@@ -572,33 +572,50 @@ def testing_nvfp4_stalled(w: Nvfp4Matrix, x: Nvfp4Matrix, y, skip_stage: int, wa
 
 # ---- weights that depend on the token (include/sq.h documents the arrays) -----
 
+_NO_DEVICE = -2  # no tensor's device (a CPU tensor's is -1)
+
+
 def _refuse(where: str, what: str, code: str = "SQ_ERR_INVALID_ARG"):
     raise SQError(STATUS_CODE[code], f"{where}: {what}")
 
 
-def _arg(t, dtype, shape, where: str, name: str) -> int:
+def _arg(t, dtype, shape, dev: int, where: str, name: str) -> int:
     """The address of a tensor argument: a contiguous CUDA tensor of this type
-    and shape on the current device, else the call is refused."""
+    and shape on the current device `dev`, else the call is refused."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     import torch
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         _refuse(where, f"{name} must be a contiguous CUDA tensor of {dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         _refuse(where, f"{name} must be {list(shape)}, got {list(t.shape)}", "SQ_ERR_SHAPE")
-    if t.get_device() != torch.cuda.current_device():
-        _refuse(where, f"{name} is not on the current device")
-    return t.data_ptr()
+    _refuse(where, f"{name} is not on the current device")
 
 
-def _opt(t, dtype, shape, where: str, name: str):
-    return None if t is None else _arg(t, dtype, shape, where, name)
+def _opt(t, dtype, shape, dev: int, where: str, name: str):
+    return None if t is None else _arg(t, dtype, shape, dev, where, name)
 
 
-def _status_arg(status, where: str):
+def _status_arg(status, dev: int, where: str):
+    if status is None:
+        return None
     import torch
-    return _opt(status, torch.int32, (1,), where, "status")
+    return _arg(status, torch.int32, (1,), dev, where, "status")
 
 
-def _workspace_arg(ws, need: int, device, where: str):
+def _stream_arg(stream, dev: int) -> int:
+    """The handle of a stream, or of the current stream of device `dev`."""
+    import torch
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (the public call costs 3 us)
+    return raw(dev) if raw else torch.cuda.current_stream().cuda_stream
+
+
+def _workspace_arg(ws, need: int, device, dev: int, where: str):
     """(tensor, address, bytes) of a uint8 workspace of at least `need` bytes;
     allocated here when the caller keeps none."""
     import torch
@@ -606,7 +623,7 @@ def _workspace_arg(ws, need: int, device, where: str):
         if not need:
             return None, None, 0
         ws = torch.empty(need, dtype=torch.uint8, device=device)
-    return ws, _arg(ws, torch.uint8, (ws.numel(),), where, "workspace"), ws.numel()
+    return ws, _arg(ws, torch.uint8, (ws.numel(),), dev, where, "workspace"), ws.numel()
 
 
 @dataclass
@@ -633,20 +650,27 @@ def route(logits, k: int, gate: str = "topk", workspace=None, status=None, pdl: 
     if logits.dim() != 2:
         _refuse("sq_route", "logits must be [T][E]", "SQ_ERR_SHAPE")
     T, E = logits.shape
-    lp = _arg(logits, torch.float32, (T, E), "sq_route", "logits")
+    cur = torch.cuda.current_device() if logits.is_cuda else _NO_DEVICE
+    lp = _arg(logits, torch.float32, (T, E), cur, "sq_route", "logits")
     if not 1 <= k <= 32 or T < 1 or T * k > 1 << 24:
         _refuse("sq_route", "T or k", "SQ_ERR_SHAPE")
     dev, i32 = logits.device, torch.int32
-    ids = torch.empty(T, k, dtype=i32, device=dev)
-    gates = torch.empty(T, k, dtype=torch.float32, device=dev)
+    if T * k % 4 == 0:  # one allocation: each array stays 16-byte aligned
+        ids, gates, order, place = torch.empty(4, T, k, dtype=i32, device=dev).unbind(0)
+        gates, order = gates.view(torch.float32), order.view(-1)
+    else:
+        ids = torch.empty(T, k, dtype=i32, device=dev)
+        gates = torch.empty(T, k, dtype=torch.float32, device=dev)
+        order = torch.empty(T * k, dtype=i32, device=dev)
+        place = torch.empty(T, k, dtype=i32, device=dev)
     offsets = torch.empty(E + 1, dtype=i32, device=dev)
-    order = torch.empty(T * k, dtype=i32, device=dev)
-    place = torch.empty(T, k, dtype=i32, device=dev)
     L = lib()
-    ws, wp, wn = _workspace_arg(workspace, int(L.sq_route_workspace_bytes(T, E, k)), dev, "sq_route")
-    _ck(L.sq_route(lp, T, E, k, SQ_GATE_ALL if gate == "all" else SQ_GATE_TOPK, ids.data_ptr(),
-                   gates.data_ptr(), offsets.data_ptr(), order.data_ptr(), place.data_ptr(), wp, wn,
-                   _status_arg(status, "sq_route"), _flags(pdl), _stream(stream)), "sq_route")
+    ws, wp, wn = _workspace_arg(workspace, L.sq_route_workspace_bytes(T, E, k), dev, cur, "sq_route")
+    rc = L.sq_route(lp, T, E, k, SQ_GATE_ALL if gate == "all" else SQ_GATE_TOPK, ids.data_ptr(),
+                    gates.data_ptr(), offsets.data_ptr(), order.data_ptr(), place.data_ptr(), wp, wn,
+                    _status_arg(status, cur, "sq_route"), _flags(pdl), _stream_arg(stream, cur))
+    if rc:
+        _ck(rc, "sq_route")
     return Route(offsets, order, place, ids, gates)
 
 
@@ -654,7 +678,8 @@ def segment(ids, S: int, workspace=None, status=None, pdl: bool = False, stream=
     """Entries with ids (int32, any shape, -1 = none) in [0, S) sorted by id."""
     import torch
     n = ids.numel()
-    ip = _arg(ids, torch.int32, tuple(ids.shape), "sq_segment", "ids")
+    cur = torch.cuda.current_device() if ids.is_cuda else _NO_DEVICE
+    ip = _arg(ids, torch.int32, ids.shape, cur, "sq_segment", "ids")
     if not 1 <= S <= 1024 or not 1 <= n <= 1 << 24:
         _refuse("sq_segment", "n or S", "SQ_ERR_SHAPE")
     dev = ids.device
@@ -662,9 +687,9 @@ def segment(ids, S: int, workspace=None, status=None, pdl: bool = False, stream=
     order = torch.empty(n, dtype=torch.int32, device=dev)
     place = torch.empty(ids.shape, dtype=torch.int32, device=dev)
     L = lib()
-    ws, wp, wn = _workspace_arg(workspace, int(L.sq_segment_workspace_bytes(n, S)), dev, "sq_segment")
+    ws, wp, wn = _workspace_arg(workspace, L.sq_segment_workspace_bytes(n, S), dev, cur, "sq_segment")
     _ck(L.sq_segment(ip, n, S, offsets.data_ptr(), order.data_ptr(), place.data_ptr(), wp, wn,
-                     _status_arg(status, "sq_segment"), _flags(pdl), _stream(stream)), "sq_segment")
+                     _status_arg(status, cur, "sq_segment"), _flags(pdl), _stream_arg(stream, cur)), "sq_segment")
     return Segments(offsets, order, place)
 
 
@@ -712,16 +737,17 @@ def experts_from_arrays(E: int, N: int, K: int, sign_bits, alpha, res_q, res_sca
     if E < 1 or E > 1024 or N < 1 or K < 1:
         _refuse(w, "E, N or K", "SQ_ERR_SHAPE")
     rows, cols = E * round_up(N, 16), round_up(K, 128)
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else _NO_DEVICE
     v = SqPackedWeight()
     v.N, v.K, v.group_size = rows, K, 128
     v.layout = SQ_LAYOUT_TILES if res_zero is None else SQ_LAYOUT_TILES_ASYM
     v.sign_stride, v.res_stride, v.scale_stride = cols // 32, cols, cols // 128
-    v.sign_bits = _arg(sign_bits, torch.int32, (rows, cols // 32), w, "sign_bits")
-    v.mask_bits = _opt(mask_bits, torch.int32, (rows, cols // 32), w, "mask_bits")
-    v.alpha = _arg(alpha, torch.float32, (rows,), w, "alpha")
-    v.res_q = _arg(res_q, torch.int8, (rows, cols), w, "res_q")
-    v.res_scale = _arg(res_scale, torch.float32, (rows, cols // 128), w, "res_scale")
-    v.res_zero = _opt(res_zero, torch.int32, (rows, cols // 128), w, "res_zero")
+    v.sign_bits = _arg(sign_bits, torch.int32, (rows, cols // 32), cur, w, "sign_bits")
+    v.mask_bits = _opt(mask_bits, torch.int32, (rows, cols // 32), cur, w, "mask_bits")
+    v.alpha = _arg(alpha, torch.float32, (rows,), cur, w, "alpha")
+    v.res_q = _arg(res_q, torch.int8, (rows, cols), cur, w, "res_q")
+    v.res_scale = _arg(res_scale, torch.float32, (rows, cols // 128), cur, w, "res_scale")
+    v.res_zero = _opt(res_zero, torch.int32, (rows, cols // 128), cur, w, "res_zero")
     e0 = SqPackedWeight()
     _ck(lib().sq_expert_view(ctypes.byref(v), E, N, 0, ctypes.byref(e0)), w)  # the library's own checks
     return PackedExperts(E, N, K, v, (sign_bits, alpha, res_q, res_scale, mask_bits, res_zero))
@@ -748,26 +774,27 @@ def grouped_linear(experts: PackedExperts, xq, sx, x_out, idx, offsets, order=No
     E, N = experts.E, experts.N
     if xq.dim() != 2:
         _refuse(w, "xq must be [rows][roundup(K,128)]", "SQ_ERR_SHAPE")
+    f32, i32, cur = torch.float32, torch.int32, torch.cuda.current_device() if xq.is_cuda else _NO_DEVICE
     rows, nout = xq.shape[0], 0 if idx is None else idx.numel()
-    xp = _arg(xq, torch.int8, (rows, experts.view.res_stride), w, "xq")
-    sp = _arg(sx, torch.float32, (rows,), w, "sx")
+    xp = _arg(xq, torch.int8, (rows, experts.view.res_stride), cur, w, "xq")
+    sp = _arg(sx, f32, (rows,), cur, w, "sx")
     op = ip = None
     if nout:
-        op = _arg(x_out, torch.float32, (rows, nout), w, "x_out")
-        ip = _arg(idx, torch.int32, (nout,), w, "idx")
+        op = _arg(x_out, f32, (rows, nout), cur, w, "x_out")
+        ip = _arg(idx, i32, (nout,), cur, w, "idx")
     n = rows if order is None else order.numel()
-    dp = _opt(order, torch.int32, (n,), w, "order")
-    fp = _arg(offsets, torch.int32, (E + 1,), w, "offsets")
+    dp = _opt(order, i32, (n,), cur, w, "order")
+    fp = _arg(offsets, i32, (E + 1,), cur, w, "offsets")
     if y is None:
-        y = torch.empty(n, N, dtype=torch.float32, device=xq.device)
-    yp = _arg(y, torch.float32, (n, N), w, "y")
+        y = torch.empty(n, N, dtype=f32, device=xq.device)
+    yp = _arg(y, f32, (n, N), cur, w, "y")
     L = lib()
-    if workspace is None:
-        workspace, wp, wn = _workspace_arg(None, grouped_workspace_bytes(experts, n), xq.device, w)
-    else:
-        wp, wn = _arg(workspace, torch.uint8, (workspace.numel(),), w, "workspace"), workspace.numel()
-    _ck(L.sq_grouped_linear(ctypes.byref(experts.view), E, N, xp, sp, op, ip, nout, rows, dp, div, fp, n, yp, wp,
-                            wn, _status_arg(status, w), _flags(pdl), _stream(stream)), w)
+    need = 0 if workspace is not None else grouped_workspace_bytes(experts, n)
+    workspace, wp, wn = _workspace_arg(workspace, need, xq.device, cur, w)
+    rc = L.sq_grouped_linear(ctypes.byref(experts.view), E, N, xp, sp, op, ip, nout, rows, dp, div, fp, n, yp, wp,
+                             wn, _status_arg(status, cur, w), _flags(pdl), _stream_arg(stream, cur))
+    if rc:
+        _ck(rc, w)
     return y
 
 
@@ -780,15 +807,18 @@ def combine(z, gates, place, base=None, out=None, status=None, pdl: bool = False
         _refuse(w, "z must be [rows][N] and gates [T][k]", "SQ_ERR_SHAPE")
     rows, N = z.shape
     T, k = gates.shape
-    zp = _arg(z, torch.float32, (rows, N), w, "z")
-    gp = _arg(gates, torch.float32, (T, k), w, "gates")
-    pp = _arg(place, torch.int32, (T, k), w, "place")
-    bp = _opt(base, torch.float32, (T, N), w, "base")
+    f32, cur = torch.float32, torch.cuda.current_device() if z.is_cuda else _NO_DEVICE
+    zp = _arg(z, f32, (rows, N), cur, w, "z")
+    gp = _arg(gates, f32, (T, k), cur, w, "gates")
+    pp = _arg(place, torch.int32, (T, k), cur, w, "place")
+    bp = _opt(base, f32, (T, N), cur, w, "base")
     if out is None:
-        out = torch.empty(T, N, dtype=torch.float32, device=z.device)
-    op = _arg(out, torch.float32, (T, N), w, "out")
-    _ck(lib().sq_combine(zp, rows, gp, pp, T, k, N, bp, op, _status_arg(status, w), _flags(pdl),
-                         _stream(stream)), w)
+        out = torch.empty(T, N, dtype=f32, device=z.device)
+    op = _arg(out, f32, (T, N), cur, w, "out")
+    rc = lib().sq_combine(zp, rows, gp, pp, T, k, N, bp, op, _status_arg(status, cur, w), _flags(pdl),
+                          _stream_arg(stream, cur))
+    if rc:
+        _ck(rc, w)
     return out
 
 
@@ -805,11 +835,12 @@ class LoraBank:
             _refuse(w, "A must be [S][R][K] and B [S][N][R], float32, float16 or bfloat16")
         self.S, self.R, self.K = A.shape
         self.N = B.shape[1]
+        cur = torch.cuda.current_device() if A.is_cuda else _NO_DEVICE
         v = SqLoraBank(S=self.S, R=self.R, K=self.K, N=self.N, type=types[A.dtype])
-        v.A = _arg(A, A.dtype, (self.S, self.R, self.K), w, "A")
-        v.B = _arg(B, A.dtype, (self.S, self.N, self.R), w, "B")
-        v.scale = _arg(scale, torch.float32, (self.S,), w, "scale")
-        v.rank = _opt(rank, torch.int32, (self.S,), w, "rank")
+        v.A = _arg(A, A.dtype, (self.S, self.R, self.K), cur, w, "A")
+        v.B = _arg(B, A.dtype, (self.S, self.N, self.R), cur, w, "B")
+        v.scale = _arg(scale, torch.float32, (self.S,), cur, w, "scale")
+        v.rank = _opt(rank, torch.int32, (self.S,), cur, w, "rank")
         self.view, self.A, self.B, self.scale, self.rank = v, A, B, scale, rank
 
 
@@ -824,18 +855,19 @@ def new_lora_workspace(bank: LoraBank, M: int, device=None):
     return torch.empty(max(lora_workspace_bytes(bank, M), 16), dtype=torch.uint8, device=device or bank.A.device)
 
 
-def _rows_arg(t, shape, where: str, name: str):
+def _rows_arg(t, shape, dev: int, where: str, name: str):
     """(address, row stride) of a float32 CUDA matrix with unit column stride."""
     import torch
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or not t.is_cuda or t.dim() != 2:
         _refuse(where, f"{name} must be a float32 CUDA matrix")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         _refuse(where, f"{name} must be {list(shape)}, got {list(t.shape)}", "SQ_ERR_SHAPE")
-    if (t.stride(1) != 1 and shape[1] > 1) or (shape[0] > 1 and t.stride(0) < shape[1]):
+    ld, step = t.stride()
+    if (step != 1 and shape[1] > 1) or (shape[0] > 1 and ld < shape[1]):
         _refuse(where, f"{name} must have unit column stride and rows that do not overlap")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         _refuse(where, f"{name} is not on the current device")
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else max(shape[1], 1)
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
 
 
 def lora_add(bank: LoraBank, x, ids, base=None, y=None, segments: Segments = None, workspace=None, status=None,
@@ -848,22 +880,23 @@ def lora_add(bank: LoraBank, x, ids, base=None, y=None, segments: Segments = Non
     if x.dim() != 2:
         _refuse(w, "x must be [M][K]", "SQ_ERR_SHAPE")
     M, N = x.shape[0], bank.N
-    xp = _arg(x, torch.float32, (M, bank.K), w, "x")
-    ip = _arg(ids, torch.int32, (M,), w, "ids")
+    cur = torch.cuda.current_device() if x.is_cuda else _NO_DEVICE
+    xp = _arg(x, torch.float32, (M, bank.K), cur, w, "x")
+    ip = _arg(ids, torch.int32, (M,), cur, w, "ids")
     if y is None:
         y = torch.empty(M, N, dtype=torch.float32, device=x.device)
-    yp, ldy = _rows_arg(y, (M, N), w, "y")
-    bp, ldb = (None, N) if base is None else _rows_arg(base, (M, N), w, "base")
+    yp, ldy = _rows_arg(y, (M, N), cur, w, "y")
+    bp, ldb = (None, N) if base is None else _rows_arg(base, (M, N), cur, w, "base")
     fp = op = None
     if segments is not None:
-        fp = _arg(segments.offsets, torch.int32, (bank.S + 1,), w, "segments.offsets")
-        op = _arg(segments.order, torch.int32, (M,), w, "segments.order")
-    if workspace is None:
-        workspace, wp, wn = _workspace_arg(None, lora_workspace_bytes(bank, M), x.device, w)
-    else:
-        wp, wn = _arg(workspace, torch.uint8, (workspace.numel(),), w, "workspace"), workspace.numel()
-    _ck(lib().sq_lora_add(ctypes.byref(bank.view), xp, M, ip, fp, op, bp, ldb, yp, ldy, wp, wn,
-                          _status_arg(status, w), _flags(pdl), _stream(stream)), w)
+        fp = _arg(segments.offsets, torch.int32, (bank.S + 1,), cur, w, "segments.offsets")
+        op = _arg(segments.order, torch.int32, (M,), cur, w, "segments.order")
+    need = 0 if workspace is not None else lora_workspace_bytes(bank, M)
+    workspace, wp, wn = _workspace_arg(workspace, need, x.device, cur, w)
+    rc = lib().sq_lora_add(ctypes.byref(bank.view), xp, M, ip, fp, op, bp, ldb, yp, ldy, wp, wn,
+                           _status_arg(status, cur, w), _flags(pdl), _stream_arg(stream, cur))
+    if rc:
+        _ck(rc, w)
     return y
 
 

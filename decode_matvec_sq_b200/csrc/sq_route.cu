@@ -322,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_place(const SegParams p) {
   const int g = threadIdx.x / S32, s = threadIdx.x % S32;
   if (g < groups && s < p.S) {
     int total = 0, before = 0;
+#pragma unroll 16
     for (int c = g; c < p.chunks; c += groups) {
       const int v = __ldg(p.counts + (int64_t)c * p.S + s);
       total += v;
