@@ -441,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOperandRegs));
     const int cw = warp - 4, gid = lane >> 2, tid4 = lane & 3;
     const bool hi = tid4 >= 2;  // takes its two 16-channel pieces in the other order
+    const int odd = (gid & 1) * 16;
     uint32_t g = 0;
     bool ok = true;
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
@@ -469,8 +470,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int c = hi ? i ^ 1 : i;  // 16 channels: words 4c .. 4c + 3
-          const uint4 u = *reinterpret_cast<const uint4*>(cb + 32 * c);
-          const uint4 v = *reinterpret_cast<const uint4*>(cb + 32 * c + 16);
+          // (odd rows read the piece's two words in the other order, so that eight
+          // neighbouring lanes read eight different 16-byte columns)
+          const uint4 e0 = *reinterpret_cast<const uint4*>(cb + 32 * c + odd);
+          const uint4 e1 = *reinterpret_cast<const uint4*>(cb + 32 * c + (odd ^ 16));
+          const uint4 u = odd ? e1 : e0, v = odd ? e0 : e1;
           uint8_t* o = ao + (((2 * tid4 + c) ^ gid) << 4);
           *reinterpret_cast<uint4*>(o) = make_uint4(u.x, u.z, v.x, v.z);
           *reinterpret_cast<uint4*>(o + 1024) = make_uint4(u.y, u.w, v.y, v.w);
