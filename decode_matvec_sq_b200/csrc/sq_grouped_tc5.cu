@@ -55,13 +55,14 @@ constexpr int kTokenUnit = 16 * kSets;  // MMA N is a multiple of this
 constexpr int kCols = kTokens / kSets, kPieces = kCols / 16;
 constexpr int kBlocks = kRows / kTileRows;
 constexpr uint32_t kTmemCols = 512; // T [0, 160), R of group g at 160 + 160 (g % 2)
-constexpr int kRawStages = 4, kStages = 2;
+constexpr int kStages = 2;
 constexpr int kABytes = kRows * kTileK;      // one operand: 16 KB
 constexpr int kBBytes = kTokens * kTileK;    // 20 KB
 constexpr int kStageBytes = 2 * kABytes + kBBytes;
 static_assert(kStageBytes % 1024 == 0 && kCols % 16 == 0 && 3 * kTokens <= (int)kTmemCols, "tile layout");
 constexpr int kMaxOut = 128;        // outlier channels this kernel takes
-constexpr int kOutPass = 8;         // of them in shared memory at a time
+constexpr int kOutHeld = 32;        // of them held in shared memory under the tile's products
+constexpr int kOutPass = 8;         // the rest: in shared memory at a time
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 template <bool MASK>
@@ -69,13 +70,15 @@ struct Raw {
   static constexpr int kSign = kBlocks * 2048;
   static constexpr int kMask = kSign + kBlocks * 256;
   static constexpr int kBytes = MASK ? kMask + kBlocks * 256 : kMask;
+  static constexpr int kStages = MASK ? 3 : 4;  // of the ring
 };
+constexpr int kRawMost = 4;
 
 struct Aux {
-  uint64_t raw_full[kRawStages], raw_empty[kRawStages];
+  uint64_t raw_full[kRawMost], raw_empty[kRawMost];
   uint64_t full[kStages], empty[kStages];
   uint64_t accf[2], acce[2];
-  uint64_t t_full, t_empty, wo_full, out, drain;
+  uint64_t t_full, t_empty, wo_full, wo_empty, out, drain;
   uint32_t tmem_base;
   int abort;
   int part[kThreads / 32];
@@ -94,7 +97,7 @@ struct Params {
   const float* xop;   // [n_out][n] outlier activations in place order
   float* wout;        // [CTAs][2][kMaxOut][kRows] outlier weights of the CTA's tiles
   int rt;             // row tiles per expert
-  int off_raw, off_xo, off_aux, off_pre, off_ostart;  // shared-memory offsets
+  int off_raw, off_xh, off_wh, off_xo, off_aux, off_pre, off_ostart;  // shared-memory offsets
 };
 
 // D (s32) (+)= A (s8) B (s8), both K-major; M = 128, N = n.  A K step of 32 bytes is
@@ -241,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kRawStages; ++s) {
+    for (int s = 0; s < RW::kStages; ++s) {
       mbar_init(&aux->raw_full[s], 1);
       mbar_init(&aux->raw_empty[s], kOperandWarps + 1);
     }
@@ -256,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&aux->t_full, 1);
     mbar_init(&aux->t_empty, kPromoteThreads / 32);
     mbar_init(&aux->wo_full, 1);
+    mbar_init(&aux->wo_empty, kPromoteThreads / 32);
     mbar_init(&aux->out, kPromoteThreads / 32);
     mbar_init(&aux->drain, 1);
     aux->abort = 0;
@@ -290,16 +294,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       // ---- raw producer: the tile's row blocks of each channel group
       uint32_t g = 0;
-      int last[kRawStages];
+      int last[RW::kStages];
 #pragma unroll
-      for (int s = 0; s < kRawStages; ++s) last[s] = -1;
+      for (int s = 0; s < RW::kStages; ++s) last[s] = -1;
       bool ok = true;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
         const Tile t = tile_at(p, pre, item);
         for (int kb = 0; kb < a.tpr; ++kb, ++g) {
-          const int s = (int)(g % kRawStages);
-          const uint32_t use = g / kRawStages;
-          if (g >= kRawStages) ok = warp_wait(&aux->raw_empty[s], (use & 1u) ^ 1u, aux, p);
+          const int s = (int)(g % RW::kStages);
+          const uint32_t use = g / RW::kStages;
+          if (g >= RW::kStages) ok = warp_wait(&aux->raw_empty[s], (use & 1u) ^ 1u, aux, p);
           ok = __all_sync(0xffffffffu, ok && !aborted(aux));
           if (!ok) break;
           uint8_t* st = smem + p.off_raw + s * RW::kBytes;
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (aborted(aux)) {  // every requested stage must have landed
 #pragma unroll
-        for (int s = 0; s < kRawStages; ++s)
+        for (int s = 0; s < RW::kStages; ++s)
           if (last[s] >= 0) (void)mbar_wait(&aux->raw_full[s], (uint32_t)last[s] & 1u, kWaitNs);
       }
     } else if (warp == 2) {
@@ -354,15 +358,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (last[s] >= 0) (void)mbar_wait(&aux->full[s], (uint32_t)last[s] & 1u, kWaitNs);
       }
     } else if (warp == 3) {
-      // ---- outlier channels: their dequantized weights for the tile's 128 rows
+      // ---- the tile's token scales and outlier channels, under its products: scales
+      // and outlier activations as rows of 160 tokens, the outlier channels'
+      // dequantized weights as rows of the tile's 128 (the first kOutHeld of them in
+      // shared memory, the rest in the CTA's scratch)
+      float* xh = reinterpret_cast<float*>(smem + p.off_xh);
+      float* wh = reinterpret_cast<float*>(smem + p.off_wh);
+      const int held = 1 + min(n_out, kOutHeld);
       uint32_t g = 0, n_items = 0;
       bool ok = true;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++n_items) {
         const Tile t = tile_at(p, pre, item);
         float* wout = p.wout + ((int64_t)blockIdx.x * 2 + (n_items & 1u)) * kMaxOut * kRows + lane;
+        if (n_items > 0) ok = warp_wait(&aux->wo_empty, (n_items & 1u) ^ 1u, aux, p);
+        if (!ok) break;
         for (int kb = 0; kb < a.tpr; ++kb, ++g) {
-          const int s = (int)(g % kRawStages);
-          ok = warp_wait(&aux->raw_full[s], (g / kRawStages) & 1u, aux, p) && !aborted(aux);
+          const int s = (int)(g % RW::kStages);
+          ok = warp_wait(&aux->raw_full[s], (g / RW::kStages) & 1u, aux, p) && !aborted(aux);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const uint8_t* st = smem + p.off_raw + s * RW::kBytes;
@@ -383,8 +395,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t mb = *reinterpret_cast<const uint32_t*>(st + RW::kMask + blk * 256 + own * 8 + 4 * R);
                 if (!((mb >> bit) & 1u)) tr = 0.0f;
               }
-              wout[o * kRows + 32 * i] = fmaf(sc, (float)code, tr);
+              const float what = fmaf(sc, (float)code, tr);
+              if (o < kOutHeld) wh[o * kRows + 32 * i + lane] = what;
+              else wout[o * kRows + 32 * i] = what;
             }
+          }
+          for (int r = kb; r < held; r += a.tpr) {  // a row of activations per group
+            const float* src = r == 0 ? p.sxp : p.xop + (int64_t)(r - 1) * a.n;
+            float v[kTokens / 32];
+#pragma unroll
+            for (int i = 0; i < kTokens / 32; ++i) v[i] = lane + 32 * i < t.cnt ? __ldg(src + t.p0 + lane + 32 * i) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kTokens / 32; ++i) xh[r * kTokens + lane + 32 * i] = v[i];
           }
           __syncwarp();
           if (lane == 0) {
@@ -446,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       for (int kb = 0; kb < a.tpr; ++kb, ++g) {
-        const int sr = (int)(g % kRawStages), sa = (int)(g % kStages);
-        ok = warp_wait(&aux->raw_full[sr], (g / kRawStages) & 1u, aux, p);
+        const int sr = (int)(g % RW::kStages), sa = (int)(g % kStages);
+        ok = warp_wait(&aux->raw_full[sr], (g / RW::kStages) & 1u, aux, p);
         if (ok && g >= kStages) ok = warp_wait(&aux->empty[sa], ((g / kStages) & 1u) ^ 1u, aux, p);
         ok = __all_sync(0xffffffffu, ok && !aborted(aux));
         if (!ok) break;
@@ -558,54 +580,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&aux->t_empty);
-      // the tile's token scales, then its outlier channels, kOutPass at a time, through
-      // shared memory: one row of 256 tokens each; this row's weights in registers
-      for (int o0 = -1; o0 < n_out; o0 += o0 < 0 ? 1 : kOutPass) {
-        const int no = o0 < 0 ? 1 : min(kOutPass, n_out - o0);
-        ok = out_sync();  // the rows of the pass before are used
-        if (!ok) break;
-        const float* src = o0 < 0 ? p.sxp : p.xop + (int64_t)o0 * a.n;
-        {
-          const int k = (int)threadIdx.x - 128 - 32 * kOperandWarps;  // a token per thread
-          static_assert(kPromoteThreads >= kTokens, "a token per thread");
-          float v[kOutPass];
+      // the token scales, the outlier channels held in shared memory, then the rest
+      // of them, kOutPass at a time: a row of tokens each, this row's weight
+      const float* xh = reinterpret_cast<const float*>(smem + p.off_xh) + t0;
+      const float* wh = reinterpret_cast<const float*>(smem + p.off_wh) + my_row;
 #pragma unroll
-          for (int o = 0; o < kOutPass; ++o)
-            v[o] = o < no && k < t.cnt ? __ldg(src + (int64_t)o * a.n + t.p0 + k) : 0.0f;
+      for (int c = 0; c < kPieces; ++c) {
+        if (16 * c >= cols) break;
+        const ulonglong2* xr = reinterpret_cast<const ulonglong2*>(xh + 16 * c);
 #pragma unroll
-          for (int o = 0; o < kOutPass; ++o)
-            if (o < no && k < kTokens) xo[o * kTokens + k] = v[o];
+        for (int i = 0; i < 4; ++i) {
+          const ulonglong2 x = xr[i];
+          F[8 * c + 2 * i] = mul2(F[8 * c + 2 * i], x.x);
+          F[8 * c + 2 * i + 1] = mul2(F[8 * c + 2 * i + 1], x.y);
         }
-        float w[kOutPass];
-#pragma unroll
-        for (int o = 0; o < kOutPass; ++o) w[o] = o0 >= 0 && o < no ? wout[(o0 + o) * kRows] : 0.0f;
-        ok = out_sync();
-        if (!ok) break;
+      }
+      auto add_row = [&](float w, const float* x0) {
+        const f32x2 w2 = pack2(w, w);
 #pragma unroll
         for (int c = 0; c < kPieces; ++c) {
           if (16 * c >= cols) break;
-          const ulonglong2* xr = reinterpret_cast<const ulonglong2*>(xo + t0 + 16 * c);
-          if (o0 < 0) {
+          const ulonglong2* xr = reinterpret_cast<const ulonglong2*>(x0 + 16 * c);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const ulonglong2 x = xr[i];
-              F[8 * c + 2 * i] = mul2(F[8 * c + 2 * i], x.x);
-              F[8 * c + 2 * i + 1] = mul2(F[8 * c + 2 * i + 1], x.y);
-            }
-          } else {
-#pragma unroll
-            for (int o = 0; o < kOutPass; ++o) {
-              if (o >= no) break;
-              const f32x2 w2 = pack2(w[o], w[o]);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const ulonglong2 x = xr[o * (kTokens / 4) + i];
-                F[8 * c + 2 * i] = fma2(w2, x.x, F[8 * c + 2 * i]);
-                F[8 * c + 2 * i + 1] = fma2(w2, x.y, F[8 * c + 2 * i + 1]);
-              }
-            }
+          for (int i = 0; i < 4; ++i) {
+            const ulonglong2 x = xr[i];
+            F[8 * c + 2 * i] = fma2(w2, x.x, F[8 * c + 2 * i]);
+            F[8 * c + 2 * i + 1] = fma2(w2, x.y, F[8 * c + 2 * i + 1]);
           }
         }
+      };
+      for (int o = 0; o < min(n_out, kOutHeld); ++o) add_row(wh[o * kRows], xh + (1 + o) * kTokens);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&aux->wo_empty);
+      for (int o0 = kOutHeld; o0 < n_out; o0 += kOutPass) {
+        const int no = min(kOutPass, n_out - o0);
+        ok = out_sync();  // the rows of the pass before are used
+        if (!ok) break;
+        const int k = (int)threadIdx.x - 128 - 32 * kOperandWarps;  // a token per thread
+        static_assert(kPromoteThreads >= kTokens, "a token per thread");
+        if (k < kTokens)
+          for (int o = 0; o < no; ++o)
+            xo[o * kTokens + k] = k < t.cnt ? __ldg(p.xop + (int64_t)(o0 + o) * a.n + t.p0 + k) : 0.0f;
+        ok = out_sync();
+        if (!ok) break;
+        for (int o = 0; o < no; ++o) add_row(wout[(o0 + o) * kRows], xo + t0 + o * kTokens);
       }
       if (!ok) break;
       if (live) {
@@ -677,7 +695,9 @@ Carve carve(int K, int64_t n, int sm_count) {
 template <bool MASK>
 cudaError_t launch_tiles(const CUtensorMap& mb, const WeightMaps& wm, Params p, int grid, cudaStream_t stream) {
   p.off_raw = kStages * kStageBytes;
-  p.off_xo = p.off_raw + kRawStages * Raw<MASK>::kBytes;
+  p.off_xh = p.off_raw + Raw<MASK>::kStages * Raw<MASK>::kBytes;
+  p.off_wh = p.off_xh + (1 + kOutHeld) * kTokens * 4;
+  p.off_xo = p.off_wh + kOutHeld * kRows * 4;
   p.off_aux = p.off_xo + kOutPass * kTokens * 4;
   p.off_pre = p.off_aux + (int)round_up(sizeof(Aux), 16);
   p.off_ostart = p.off_pre + (int)round_up(4 * (p.a.E + 1), 16);
