@@ -62,7 +62,9 @@ constexpr int kStageBytes = 2 * kABytes + kBBytes;
 static_assert(kStageBytes % 1024 == 0 && kCols % 16 == 0 && 3 * kTokens <= (int)kTmemCols, "tile layout");
 constexpr int kMaxOut = 128;        // outlier channels this kernel takes
 constexpr int kOutHeld = 32;        // of them held in shared memory under the tile's products
-constexpr int kOutPass = 8;         // the rest: in shared memory at a time
+// row strides of the held activations and weights (8 mod 32: the four rows a quad's
+// lanes read fall into different banks) and of a warp's 8 columns of their products
+constexpr int kXhStride = kTokens + 8, kWhStride = kRows + 8, kUStride = 36;
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 template <bool MASK>
@@ -70,9 +72,9 @@ struct Raw {
   static constexpr int kSign = kBlocks * 2048;
   static constexpr int kMask = kSign + kBlocks * 256;
   static constexpr int kBytes = MASK ? kMask + kBlocks * 256 : kMask;
-  static constexpr int kStages = MASK ? 3 : 4;  // of the ring
+  static constexpr int kStages = 3;  // of the ring
 };
-constexpr int kRawMost = 4;
+constexpr int kRawMost = 3;
 
 struct Aux {
   uint64_t raw_full[kRawMost], raw_empty[kRawMost];
@@ -97,7 +99,7 @@ struct Params {
   const float* xop;   // [n_out][n] outlier activations in place order
   float* wout;        // [CTAs][2][kMaxOut][kRows] outlier weights of the CTA's tiles
   int rt;             // row tiles per expert
-  int off_raw, off_xh, off_wh, off_xo, off_aux, off_pre, off_ostart;  // shared-memory offsets
+  int off_raw, off_xh, off_wh, off_u, off_aux, off_pre, off_ostart, off_oj;  // shared-memory offsets
 };
 
 // D (s32) (+)= A (s8) B (s8), both K-major; M = 128, N = n.  A K step of 32 bytes is
@@ -196,6 +198,11 @@ __device__ __forceinline__ float2 unpack2(f32x2 v) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
   return f;
 }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
   f32x2 d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -206,6 +213,18 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+// v = hi + lo: hi rounded to tf32's 11 bits, lo the exact rest; one k8 step on tf32.
+__device__ __forceinline__ void cut_tf32(float v, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(v));
+  lo = __float_as_uint(v - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
 // One tile: an expert's 128 rows x up to 256 of its places.
 struct Tile {
   int rb0;       // first row block in the stack
@@ -240,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Aux* aux = reinterpret_cast<Aux*>(smem + p.off_aux);
   int* pre = reinterpret_cast<int*>(smem + p.off_pre);
   int* ostart = reinterpret_cast<int*>(smem + p.off_ostart);
+  uint8_t* oj = smem + p.off_oj;  // the outlier channels in their groups
   const GroupedArgs& a = p.a;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -277,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int i = threadIdx.x; i < n_out; i += kThreads) {
     const int g0 = i > 0 ? (__ldg(a.idx + i - 1) >> 7) + 1 : 0, g1 = __ldg(a.idx + i) >> 7;
     for (int g = g0; g <= g1; ++g) ostart[g] = i;
+    oj[i] = (uint8_t)(__ldg(a.idx + i) & 127);
   }
   for (int g = (n_out > 0 ? (__ldg(a.idx + n_out - 1) >> 7) + 1 : 0) + threadIdx.x; g <= a.tpr; g += kThreads)
     ostart[g] = n_out;
@@ -365,11 +386,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* xh = reinterpret_cast<float*>(smem + p.off_xh);
       float* wh = reinterpret_cast<float*>(smem + p.off_wh);
       const int held = 1 + min(n_out, kOutHeld);
+      // rows up to the next eight channels are zero
+      for (int r = held; r < 1 + (held + 6) / 8 * 8; ++r) {
+        for (int i = lane; i < kTokens; i += 32) xh[r * kXhStride + i] = 0.0f;
+        for (int i = lane; i < kRows; i += 32) wh[(r - 1) * kWhStride + i] = 0.0f;
+      }
       uint32_t g = 0, n_items = 0;
       bool ok = true;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++n_items) {
         const Tile t = tile_at(p, pre, item);
         float* wout = p.wout + ((int64_t)blockIdx.x * 2 + (n_items & 1u)) * kMaxOut * kRows + lane;
+        // this lane's rows: 32 i + lane of the tile; their trunk scales, and the group
+        // scales of the next group that has an outlier, loaded a group ahead
+        float al[4], sc[4];
+        auto group_scales = [&](int kb) {
+          if (ostart[kb + 1] > ostart[kb])
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              sc[i] = __ldg(a.scale + ((t.rb0 + min(2 * i + (lane >> 4), t.blocks - 1)) * (int64_t)a.tpr + kb) * kTileRows + (lane & 15));
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          al[i] = __ldg(a.alpha + (t.rb0 + min(2 * i + (lane >> 4), t.blocks - 1)) * (int64_t)kTileRows + (lane & 15));
+        group_scales(0);
         if (n_items > 0) ok = warp_wait(&aux->wo_empty, (n_items & 1u) ^ 1u, aux, p);
         if (!ok) break;
         for (int kb = 0; kb < a.tpr; ++kb, ++g) {
@@ -379,41 +418,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           const uint8_t* st = smem + p.off_raw + s * RW::kBytes;
           for (int o = ostart[kb]; o < ostart[kb + 1]; ++o) {
-            const int j = __ldg(a.idx + o) & 127, w = (j & 31) >> 2, bit = tiled_bit_of(j & 31);
+            const int j = oj[o], w = (j & 31) >> 2, bit = tiled_bit_of(j & 31);
             const int own = (lane & 7) * 4 + (j >> 5), R = (lane >> 3) & 1;  // rows lane % 16 of a block
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int blk = 2 * i + (lane >> 4);
-              const int64_t rb = t.rb0 + min(blk, t.blocks - 1);
-              const float al = __ldg(a.alpha + rb * kTileRows + (lane & 15));
-              const float sc = __ldg(a.scale + (rb * a.tpr + kb) * kTileRows + (lane & 15));
               const int code = reinterpret_cast<const int8_t*>(
                   st)[blk * 2048 + own * 64 + (w >> 1) * 16 + ((w & 1) * 2 + R) * 4 + (j & 3)];
               const uint32_t sb = *reinterpret_cast<const uint32_t*>(st + RW::kSign + blk * 256 + own * 8 + 4 * R);
-              float tr = ((sb >> bit) & 1u) ? al : -al;
+              float tr = ((sb >> bit) & 1u) ? al[i] : -al[i];
               if constexpr (MASK) {
                 const uint32_t mb = *reinterpret_cast<const uint32_t*>(st + RW::kMask + blk * 256 + own * 8 + 4 * R);
                 if (!((mb >> bit) & 1u)) tr = 0.0f;
               }
-              const float what = fmaf(sc, (float)code, tr);
-              if (o < kOutHeld) wh[o * kRows + 32 * i + lane] = what;
+              const float what = fmaf(sc[i], (float)code, tr);
+              if (o < kOutHeld) wh[o * kWhStride + 32 * i + lane] = what;
               else wout[o * kRows + 32 * i] = what;
             }
           }
-          for (int r = kb; r < held; r += a.tpr) {  // a row of activations per group
-            const float* src = r == 0 ? p.sxp : p.xop + (int64_t)(r - 1) * a.n;
-            float v[kTokens / 32];
-#pragma unroll
-            for (int i = 0; i < kTokens / 32; ++i) v[i] = lane + 32 * i < t.cnt ? __ldg(src + t.p0 + lane + 32 * i) : 0.0f;
-#pragma unroll
-            for (int i = 0; i < kTokens / 32; ++i) xh[r * kTokens + lane + 32 * i] = v[i];
-          }
+          if (kb + 1 < a.tpr) group_scales(kb + 1);
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&aux->raw_empty[s]);
-            if (kb == a.tpr - 1) mbar_arrive(&aux->wo_full);
+          if (lane == 0) mbar_arrive(&aux->raw_empty[s]);
+          // a row of tokens per group (zero past the tile's), waited for at the tile's end
+          for (int r = kb; r < held; r += a.tpr) {
+            const float* src = (r == 0 ? p.sxp : p.xop + (int64_t)(r - 1) * a.n) + t.p0;
+            const uint32_t dst = smem_u32(xh + r * kXhStride + lane);
+#pragma unroll
+            for (int i = 0; i < kTokens / 32; ++i) {
+              const bool in = lane + 32 * i < t.cnt;
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 128 * i),
+                           "l"(in ? src + lane + 32 * i : src), "r"(in ? 4 : 0) : "memory");
+            }
           }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&aux->wo_full);
       }
     } else if (warp == 1) {
       // ---- MMA issuer (the whole warp walks; one lane issues)
@@ -526,7 +566,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int set = (warp - 4 - kOperandWarps) >> 2, q = warp & 3;  // half of the tokens; tensor-memory lane quarter
     const int my_row = 32 * q + lane;
     uint32_t g = 0, n_items = 0, n_sync = 0;
-    float* xo = reinterpret_cast<float*>(smem + p.off_xo);
     bool ok = true;
     // a barrier of these warps, with a bounded wait
     auto out_sync = [&]() -> bool {
@@ -537,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++n_items) {
       const Tile t = tile_at(p, pre, item);
       const int cols = t.n / kSets;
-      const float* wout = p.wout + ((int64_t)blockIdx.x * 2 + (n_items & 1u)) * kMaxOut * kRows + my_row;
+      const float* wout = p.wout + ((int64_t)blockIdx.x * 2 + (n_items & 1u)) * kMaxOut * kRows;
       f32x2 F[kCols / 2];  // this row's sums, two tokens each
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) F[i] = 0ull;
@@ -581,9 +620,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&aux->t_empty);
       // the token scales, the outlier channels held in shared memory, then the rest
-      // of them, kOutPass at a time: a row of tokens each, this row's weight
-      const float* xh = reinterpret_cast<const float*>(smem + p.off_xh) + t0;
-      const float* wh = reinterpret_cast<const float*>(smem + p.off_wh) + my_row;
+      // of them
+      float* xh_all = reinterpret_cast<float*>(smem + p.off_xh);
+      float* wh_all = reinterpret_cast<float*>(smem + p.off_wh);
+      const float *xh = xh_all + t0, *wh = wh_all + 32 * q;
 #pragma unroll
       for (int c = 0; c < kPieces; ++c) {
         if (16 * c >= cols) break;
@@ -595,37 +635,83 @@ __global__ void __launch_bounds__(kThreads, 1)
           F[8 * c + 2 * i + 1] = mul2(F[8 * c + 2 * i + 1], x.y);
         }
       }
-      auto add_row = [&](float w, const float* x0) {
-        const f32x2 w2 = pack2(w, w);
+      // Outlier channels by the tensor cores (mma.sync, tf32): What (rows of w0) and x
+      // (rows of x0) of `no` channels cut into two parts each, the products of parts but
+      // the smallest summed in binary32; 16 tokens at a time, from the accumulators' layout to a row per lane through
+      // shared memory.  (A row per lane on the CUDA cores needs each activation
+      // broadcast to all lanes: 950 clocks per channel and tile against 150.)
+      auto add_channels = [&](int no) {
+        const float *w0 = wh, *x0 = xh + kXhStride;
+        float* ub = reinterpret_cast<float*>(smem + p.off_u) + (warp - 4 - kOperandWarps) * 8 * kUStride;
+        const int gid = lane >> 2, tid4 = lane & 3;
 #pragma unroll
         for (int c = 0; c < kPieces; ++c) {
           if (16 * c >= cols) break;
-          const ulonglong2* xr = reinterpret_cast<const ulonglong2*>(x0 + 16 * c);
+          float acc[2][2][4] = {};
+          for (int k = 0; k < no; k += 8) {
+            uint32_t ah[2][4], al[2][4], bh[2][2], bl[2][2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const ulonglong2 x = xr[i];
-            F[8 * c + 2 * i] = fma2(w2, x.x, F[8 * c + 2 * i]);
-            F[8 * c + 2 * i + 1] = fma2(w2, x.y, F[8 * c + 2 * i + 1]);
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int o = k + tid4 + 4 * (i >> 1);
+                cut_tf32(w0[o * kWhStride + 16 * m + gid + 8 * (i & 1)], ah[m][i], al[m][i]);
+              }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int o = k + tid4 + 4 * i;
+                cut_tf32(x0[o * kXhStride + 16 * c + 8 * j + gid], bh[j][i], bl[j][i]);
+              }
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                mma_tf32(acc[m][j], al[m], bh[j]);
+                mma_tf32(acc[m][j], ah[m], bl[j]);
+                mma_tf32(acc[m][j], ah[m], bh[j]);
+              }
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                ub[(2 * tid4 + (i & 1)) * kUStride + 16 * m + gid + 8 * (i >> 1)] = acc[m][j][i];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              F[8 * c + 4 * j + i] =
+                  add2(F[8 * c + 4 * j + i], pack2(ub[2 * i * kUStride + lane], ub[(2 * i + 1) * kUStride + lane]));
+            __syncwarp();
           }
         }
       };
-      for (int o = 0; o < min(n_out, kOutHeld); ++o) add_row(wh[o * kRows], xh + (1 + o) * kTokens);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&aux->wo_empty);
-      for (int o0 = kOutHeld; o0 < n_out; o0 += kOutPass) {
-        const int no = min(kOutPass, n_out - o0);
-        ok = out_sync();  // the rows of the pass before are used
+      if (n_out > 0) add_channels(min(n_out, kOutHeld));
+      // channels past the held ones: kOutHeld at a time into the same place
+      for (int o0 = kOutHeld; o0 < n_out; o0 += kOutHeld) {
+        const int no = min(kOutHeld, n_out - o0);
+        ok = out_sync();  // the channels before are used
         if (!ok) break;
-        const int k = (int)threadIdx.x - 128 - 32 * kOperandWarps;  // a token per thread
-        static_assert(kPromoteThreads >= kTokens, "a token per thread");
-        if (k < kTokens)
-          for (int o = 0; o < no; ++o)
-            xo[o * kTokens + k] = k < t.cnt ? __ldg(p.xop + (int64_t)(o0 + o) * a.n + t.p0 + k) : 0.0f;
+        const int k = (int)threadIdx.x - 128 - 32 * kOperandWarps;
+        static_assert(kPromoteThreads == 2 * kRows && kPromoteThreads >= kTokens, "two rows of weights a pass, a token per thread");
+        const int no8 = (no + 7) & ~7;  // (zero up to the next eight)
+#pragma unroll 8
+        for (int o = 0; o < no8; ++o)
+          if (k < kTokens)
+            xh_all[(1 + o) * kXhStride + k] = o < no && k < t.cnt ? __ldg(p.xop + (int64_t)(o0 + o) * a.n + t.p0 + k) : 0.0f;
+#pragma unroll 8
+        for (int o = k / kRows; o < no8; o += 2)
+          wh_all[o * kWhStride + k % kRows] = o < no ? wout[(o0 + o) * kRows + k % kRows] : 0.0f;
         ok = out_sync();
         if (!ok) break;
-        for (int o = 0; o < no; ++o) add_row(wout[(o0 + o) * kRows], xo + t0 + o * kTokens);
+        add_channels(no);
       }
       if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&aux->wo_empty);
       if (live) {
         float* yr = a.y + (int64_t)(t.p0 + t0) * a.N + row;
 #pragma unroll
@@ -696,12 +782,13 @@ template <bool MASK>
 cudaError_t launch_tiles(const CUtensorMap& mb, const WeightMaps& wm, Params p, int grid, cudaStream_t stream) {
   p.off_raw = kStages * kStageBytes;
   p.off_xh = p.off_raw + Raw<MASK>::kStages * Raw<MASK>::kBytes;
-  p.off_wh = p.off_xh + (1 + kOutHeld) * kTokens * 4;
-  p.off_xo = p.off_wh + kOutHeld * kRows * 4;
-  p.off_aux = p.off_xo + kOutPass * kTokens * 4;
+  p.off_wh = p.off_xh + (1 + kOutHeld) * kXhStride * 4;
+  p.off_u = p.off_wh + kOutHeld * kWhStride * 4;
+  p.off_aux = p.off_u + kPromoteThreads / 32 * 8 * kUStride * 4;
   p.off_pre = p.off_aux + (int)round_up(sizeof(Aux), 16);
   p.off_ostart = p.off_pre + (int)round_up(4 * (p.a.E + 1), 16);
-  const int smem = p.off_ostart + (int)round_up(4 * (p.a.tpr + 1), 16) + 1024;
+  p.off_oj = p.off_ostart + 4 * (p.a.tpr + 1);
+  const int smem = (int)round_up(p.off_oj + kMaxOut, 16) + 1024;
   if (smem > 227 * 1024) return cudaErrorInvalidValue;
   auto* fn = k_grouped_tc5<MASK>;
   // the register split of the warpgroups must add up to the launch's registers
