@@ -62,9 +62,8 @@ constexpr int kStageBytes = 2 * kABytes + kBBytes;
 static_assert(kStageBytes % 1024 == 0 && kCols % 16 == 0 && 3 * kTokens <= (int)kTmemCols, "tile layout");
 constexpr int kMaxOut = 128;        // outlier channels this kernel takes
 constexpr int kOutHeld = 32;        // of them held in shared memory under the tile's products
-// row strides of the held activations and weights (8 mod 32: the four rows a quad's
-// lanes read fall into different banks) and of a warp's 8 columns of their products
-constexpr int kXhStride = kTokens + 8, kWhStride = kRows + 8, kUStride = 36;
+constexpr int kOutChunk = 16;       // of them in one stage
+
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 template <bool MASK>
@@ -72,15 +71,15 @@ struct Raw {
   static constexpr int kSign = kBlocks * 2048;
   static constexpr int kMask = kSign + kBlocks * 256;
   static constexpr int kBytes = MASK ? kMask + kBlocks * 256 : kMask;
-  static constexpr int kStages = 3;  // of the ring
+  static constexpr int kStages = MASK ? 3 : 4;  // of the ring
 };
-constexpr int kRawMost = 3;
+constexpr int kRawMost = 4;
 
 struct Aux {
   uint64_t raw_full[kRawMost], raw_empty[kRawMost];
   uint64_t full[kStages], empty[kStages];
   uint64_t accf[2], acce[2];
-  uint64_t t_full, t_empty, wo_full, wo_empty, out, drain;
+  uint64_t t_full, t_empty, wo_full, wo_empty, drain;
   uint32_t tmem_base;
   int abort;
   int part[kThreads / 32];
@@ -96,10 +95,9 @@ struct WeightMaps {
 struct Params {
   GroupedArgs a;
   const float* sxp;   // [n] token scales in place order
-  const float* xop;   // [n_out][n] outlier activations in place order
-  float* wout;        // [CTAs][2][kMaxOut][kRows] outlier weights of the CTA's tiles
+  float* wout;        // [CTAs][kMaxOut][kRows] outlier weights of the CTA's tile
   int rt;             // row tiles per expert
-  int off_raw, off_xh, off_wh, off_u, off_aux, off_pre, off_ostart, off_oj;  // shared-memory offsets
+  int off_raw, off_sx, off_wh, off_aux, off_pre, off_ostart, off_oj;  // shared-memory offsets
 };
 
 // D (s32) (+)= A (s8) B (s8), both K-major; M = 128, N = n.  A K step of 32 bytes is
@@ -113,6 +111,26 @@ __device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint3
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0));
+}
+
+// D (f32) (+)= A (tf32) B (tf32); a K step of 8 is 32 bytes too.
+__device__ __forceinline__ uint32_t idesc_tf32_of(int n) {
+  return (1u << 4) | (2u << 7) | (2u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+__device__ __forceinline__ void mma_tf32(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::tf32 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0));
+}
+// v = hi + lo: hi rounded to tf32's 11 bits, lo the exact rest (of which the tensor
+// cores read 11 bits).
+__device__ __forceinline__ void cut_tf32(float v, float& hi, float& lo) {
+  uint32_t h;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(h) : "f"(v));
+  hi = __uint_as_float(h);
+  lo = v - hi;
 }
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Aux* aux, const Params& p) {
@@ -213,18 +231,6 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
-// v = hi + lo: hi rounded to tf32's 11 bits, lo the exact rest; one k8 step on tf32.
-__device__ __forceinline__ void cut_tf32(float v, uint32_t& hi, uint32_t& lo) {
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(v));
-  lo = __float_as_uint(v - __uint_as_float(hi));
-}
-__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
-
 // One tile: an expert's 128 rows x up to 256 of its places.
 struct Tile {
   int rb0;       // first row block in the stack
@@ -252,7 +258,8 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const int* pre, int ite
 }
 template <bool MASK>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_grouped_tc5(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ WeightMaps wm, const Params p) {
+    k_grouped_tc5(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmX,
+                  const __grid_constant__ WeightMaps wm, const Params p) {
   using RW = Raw<MASK>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -279,8 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&aux->t_full, 1);
     mbar_init(&aux->t_empty, kPromoteThreads / 32);
     mbar_init(&aux->wo_full, 1);
-    mbar_init(&aux->wo_empty, kPromoteThreads / 32);
-    mbar_init(&aux->out, kPromoteThreads / 32);
+    mbar_init(&aux->wo_empty, kOperandWarps + kPromoteThreads / 32);
     mbar_init(&aux->drain, 1);
     aux->abort = 0;
     fence_barrier_init();
@@ -294,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bad |= j < 0 || j >= a.K || jp >= j;
   }
   const int n_out = __syncthreads_or(bad) ? 0 : a.n_out;
+  const int steps = a.tpr + (n_out + kOutChunk - 1) / kOutChunk;  // of a tile: channel groups, outlier chunks
   for (int i = threadIdx.x; i < n_out; i += kThreads) {
     const int g0 = i > 0 ? (__ldg(a.idx + i - 1) >> 7) + 1 : 0, g1 = __ldg(a.idx + i) >> 7;
     for (int g = g0; g <= g1; ++g) ostart[g] = i;
@@ -346,7 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (last[s] >= 0) (void)mbar_wait(&aux->raw_full[s], (uint32_t)last[s] & 1u, kWaitNs);
       }
     } else if (warp == 2) {
-      // ---- activation producer: n rows of 128 codes per channel group
+      // ---- activation producer: n rows of 128 codes per channel group, of 32
+      // binary32 values per outlier chunk (16 channels' first parts, their second)
       uint32_t g = 0;
       int last[kStages];
 #pragma unroll
@@ -354,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
         const Tile t = tile_at(p, pre, item);
-        for (int kb = 0; kb < a.tpr; ++kb, ++g) {
+        for (int kb = 0; kb < steps; ++kb, ++g) {
           const int s = (int)(g % kStages);
           const uint32_t use = g / kStages;
           if (g >= kStages) ok = warp_wait(&aux->empty[s], (use & 1u) ^ 1u, aux, p);
@@ -364,7 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) {
             mbar_arrive_expect_tx(&aux->full[s], (uint32_t)t.n * kTileK);
             for (int r = 0; r < t.n; r += kTokenUnit)
-              tc05::tma_load_2d(st + r * kTileK, &tmB, kb * kTileK, t.p0 + r, &aux->full[s]);
+              if (kb < a.tpr)
+                tc05::tma_load_2d(st + r * kTileK, &tmB, kb * kTileK, t.p0 + r, &aux->full[s]);
+              else
+                tc05::tma_load_2d(st + r * kTileK, &tmX, 0, (kb - a.tpr) * a.n + t.p0 + r, &aux->full[s]);
           }
           __syncwarp();
           last[s] = (int)use;
@@ -379,31 +390,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (last[s] >= 0) (void)mbar_wait(&aux->full[s], (uint32_t)last[s] & 1u, kWaitNs);
       }
     } else if (warp == 3) {
-      // ---- the tile's token scales and outlier channels, under its products: scales
-      // and outlier activations as rows of 160 tokens, the outlier channels'
+      // ---- under the tile's products: its token scales, and the outlier channels'
       // dequantized weights as rows of the tile's 128 (the first kOutHeld of them in
       // shared memory, the rest in the CTA's scratch)
-      float* xh = reinterpret_cast<float*>(smem + p.off_xh);
+      float* sxh = reinterpret_cast<float*>(smem + p.off_sx);
       float* wh = reinterpret_cast<float*>(smem + p.off_wh);
-      const int held = 1 + min(n_out, kOutHeld);
-      // rows up to the next eight channels are zero
-      for (int r = held; r < 1 + (held + 6) / 8 * 8; ++r) {
-        for (int i = lane; i < kTokens; i += 32) xh[r * kXhStride + i] = 0.0f;
-        for (int i = lane; i < kRows; i += 32) wh[(r - 1) * kWhStride + i] = 0.0f;
-      }
+      float* wout = p.wout + (int64_t)blockIdx.x * kMaxOut * kRows + lane;
       uint32_t g = 0, n_items = 0;
       bool ok = true;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++n_items) {
         const Tile t = tile_at(p, pre, item);
-        float* wout = p.wout + ((int64_t)blockIdx.x * 2 + (n_items & 1u)) * kMaxOut * kRows + lane;
         // this lane's rows: 32 i + lane of the tile; their trunk scales, and the group
-        // scales of the next group that has an outlier, loaded a group ahead
+        // scales of the next group, loaded a group ahead
         float al[4], sc[4];
         auto group_scales = [&](int kb) {
-          if (ostart[kb + 1] > ostart[kb])
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              sc[i] = __ldg(a.scale + ((t.rb0 + min(2 * i + (lane >> 4), t.blocks - 1)) * (int64_t)a.tpr + kb) * kTileRows + (lane & 15));
+          for (int i = 0; i < 4; ++i)
+            sc[i] = __ldg(a.scale + ((t.rb0 + min(2 * i + (lane >> 4), t.blocks - 1)) * (int64_t)a.tpr + kb) * kTileRows + (lane & 15));
         };
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -411,6 +414,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         group_scales(0);
         if (n_items > 0) ok = warp_wait(&aux->wo_empty, (n_items & 1u) ^ 1u, aux, p);
         if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < kTokens / 32; ++i) {  // (waited for at the tile's end; zero past its tokens)
+          const bool in = lane + 32 * i < t.cnt;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(sxh + lane + 32 * i)),
+                       "l"(p.sxp + t.p0 + (in ? lane + 32 * i : 0)), "r"(in ? 4 : 0) : "memory");
+        }
         for (int kb = 0; kb < a.tpr; ++kb, ++g) {
           const int s = (int)(g % RW::kStages);
           ok = warp_wait(&aux->raw_full[s], (g / RW::kStages) & 1u, aux, p) && !aborted(aux);
@@ -432,24 +441,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!((mb >> bit) & 1u)) tr = 0.0f;
               }
               const float what = fmaf(sc[i], (float)code, tr);
-              if (o < kOutHeld) wh[o * kWhStride + 32 * i + lane] = what;
+              if (o < kOutHeld) wh[o * kRows + 32 * i + lane] = what;
               else wout[o * kRows + 32 * i] = what;
             }
           }
           if (kb + 1 < a.tpr) group_scales(kb + 1);
           __syncwarp();
           if (lane == 0) mbar_arrive(&aux->raw_empty[s]);
-          // a row of tokens per group (zero past the tile's), waited for at the tile's end
-          for (int r = kb; r < held; r += a.tpr) {
-            const float* src = (r == 0 ? p.sxp : p.xop + (int64_t)(r - 1) * a.n) + t.p0;
-            const uint32_t dst = smem_u32(xh + r * kXhStride + lane);
-#pragma unroll
-            for (int i = 0; i < kTokens / 32; ++i) {
-              const bool in = lane + 32 * i < t.cnt;
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 128 * i),
-                           "l"(in ? src + lane + 32 * i : src), "r"(in ? 4 : 0) : "memory");
-            }
-          }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
@@ -462,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t s0 = smem_u32(smem);
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++n_items) {
         const Tile t = tile_at(p, pre, item);
-        const uint32_t idesc = idesc_of(t.n);
-        for (int kb = 0; kb < a.tpr; ++kb, ++g) {
+        const uint32_t idesc = idesc_of(t.n), idesc_x = idesc_tf32_of(t.n);
+        for (int kb = 0; kb < steps; ++kb, ++g) {
           const int s = (int)(g % kStages), b = (int)(g & 1u);
           ok = warp_wait(&aux->full[s], (g / kStages) & 1u, aux, p) &&
                (g < 2 || warp_wait(&aux->acce[b], ((g >> 1) & 1u) ^ 1u, aux, p));
@@ -472,6 +470,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t da = tc05::sw128_desc(s0 + s * kStageBytes);
           const uint64_t dt = da + (kABytes >> 4), db = da + (2 * kABytes >> 4);
           const uint32_t d = tmem + kTokens + kTokens * b;
+          if (kb >= a.tpr) {  // What (first | first parts) x (first | second), What (second) x (first)
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) mma_tf32(d, da + 2 * kk, db + 2 * kk, idesc_x, kk > 0);
+#pragma unroll
+              for (int kk = 0; kk < 2; ++kk) mma_tf32(d, dt + 2 * kk, db + 2 * kk, idesc_x, true);
+              tc05::mma_commit(&aux->accf[b]);
+              tc05::mma_commit(&aux->empty[s]);
+            }
+            __syncwarp();
+            continue;
+          }
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) mma_i8(d, da + 2 * kk, db + 2 * kk, idesc, kk > 0);
@@ -504,12 +514,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cw = warp - 4, gid = lane >> 2, tid4 = lane & 3;
     const bool hi = tid4 >= 2;  // takes its two 16-channel pieces in the other order
     const int odd = (gid & 1) * 16;
-    uint32_t g = 0;
+    uint32_t g = 0, rg = 0, n_items = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      for (int kb = 0; kb < a.tpr; ++kb, ++g) {
-        const int sr = (int)(g % RW::kStages), sa = (int)(g % kStages);
-        ok = warp_wait(&aux->raw_full[sr], (g / RW::kStages) & 1u, aux, p);
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++n_items) {
+      for (int kb = 0; kb < a.tpr; ++kb, ++g, ++rg) {
+        const int sr = (int)(rg % RW::kStages), sa = (int)(g % kStages);
+        ok = warp_wait(&aux->raw_full[sr], (rg / RW::kStages) & 1u, aux, p);
         if (ok && g >= kStages) ok = warp_wait(&aux->empty[sa], ((g / kStages) & 1u) ^ 1u, aux, p);
         ok = __all_sync(0xffffffffu, ok && !aborted(aux));
         if (!ok) break;
@@ -555,6 +565,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&aux->raw_empty[sr]);
         }
       }
+      if (!ok) break;
+      // the outlier chunks: What of 16 channels cut in two, 8 channels of a row per thread
+      ok = warp_wait(&aux->wo_full, n_items & 1u, aux, p);
+      if (!ok) break;
+      const float* wout = p.wout + (int64_t)blockIdx.x * kMaxOut * kRows;
+      const float* wh = reinterpret_cast<const float*>(smem + p.off_wh);
+      const int row = ((cw & 3) << 5) + lane, half = cw >> 2;
+      for (int o0 = 8 * half; o0 < (steps - a.tpr) * kOutChunk; o0 += kOutChunk, ++g) {
+        const int sa = (int)(g % kStages);
+        if (g >= kStages) ok = warp_wait(&aux->empty[sa], ((g / kStages) & 1u) ^ 1u, aux, p);
+        ok = __all_sync(0xffffffffu, ok && !aborted(aux));
+        if (!ok) break;
+        const float* src = (o0 < kOutHeld ? wh : wout) + o0 * kRows + row;
+        float h[8], l[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cut_tf32(o0 + i < n_out ? src[i * kRows] : 0.0f, h[i], l[i]);
+        uint8_t* ao = smem + sa * kStageBytes + row * 128;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int at = ((2 * half + i) ^ (row & 7)) << 4;
+          const float4 hv = make_float4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+          *reinterpret_cast<float4*>(ao + at) = hv;
+          *reinterpret_cast<float4*>(ao + (at ^ 64)) = hv;
+          *reinterpret_cast<float4*>(ao + kABytes + at) = make_float4(l[4 * i], l[4 * i + 1], l[4 * i + 2], l[4 * i + 3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&aux->full[sa]);
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&aux->wo_empty);
     }
     // winding down after a timeout: the activation producer waits for the copies of
     // the stages it has requested, on barriers that count these warps too
@@ -565,18 +607,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPromoteRegs));
     const int set = (warp - 4 - kOperandWarps) >> 2, q = warp & 3;  // half of the tokens; tensor-memory lane quarter
     const int my_row = 32 * q + lane;
-    uint32_t g = 0, n_items = 0, n_sync = 0;
+    uint32_t g = 0, n_items = 0;
     bool ok = true;
-    // a barrier of these warps, with a bounded wait
-    auto out_sync = [&]() -> bool {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&aux->out);
-      return warp_wait(&aux->out, n_sync++ & 1u, aux, p);
-    };
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++n_items) {
       const Tile t = tile_at(p, pre, item);
       const int cols = t.n / kSets;
-      const float* wout = p.wout + ((int64_t)blockIdx.x * 2 + (n_items & 1u)) * kMaxOut * kRows;
       f32x2 F[kCols / 2];  // this row's sums, two tokens each
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) F[i] = 0ull;
@@ -619,15 +654,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&aux->t_empty);
-      // the token scales, the outlier channels held in shared memory, then the rest
-      // of them
-      float* xh_all = reinterpret_cast<float*>(smem + p.off_xh);
-      float* wh_all = reinterpret_cast<float*>(smem + p.off_wh);
-      const float *xh = xh_all + t0, *wh = wh_all + 32 * q;
+      const float* sxh = reinterpret_cast<const float*>(smem + p.off_sx) + t0;
 #pragma unroll
       for (int c = 0; c < kPieces; ++c) {
         if (16 * c >= cols) break;
-        const ulonglong2* xr = reinterpret_cast<const ulonglong2*>(xh + 16 * c);
+        const ulonglong2* xr = reinterpret_cast<const ulonglong2*>(sxh + 16 * c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const ulonglong2 x = xr[i];
@@ -635,83 +666,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           F[8 * c + 2 * i + 1] = mul2(F[8 * c + 2 * i + 1], x.y);
         }
       }
-      // Outlier channels by the tensor cores (mma.sync, tf32): What (rows of w0) and x
-      // (rows of x0) of `no` channels cut into two parts each, the products of parts but
-      // the smallest summed in binary32; 16 tokens at a time, from the accumulators' layout to a row per lane through
-      // shared memory.  (A row per lane on the CUDA cores needs each activation
-      // broadcast to all lanes: 950 clocks per channel and tile against 150.)
-      auto add_channels = [&](int no) {
-        const float *w0 = wh, *x0 = xh + kXhStride;
-        float* ub = reinterpret_cast<float*>(smem + p.off_u) + (warp - 4 - kOperandWarps) * 8 * kUStride;
-        const int gid = lane >> 2, tid4 = lane & 3;
-#pragma unroll
-        for (int c = 0; c < kPieces; ++c) {
-          if (16 * c >= cols) break;
-          float acc[2][2][4] = {};
-          for (int k = 0; k < no; k += 8) {
-            uint32_t ah[2][4], al[2][4], bh[2][2], bl[2][2];
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int o = k + tid4 + 4 * (i >> 1);
-                cut_tf32(w0[o * kWhStride + 16 * m + gid + 8 * (i & 1)], ah[m][i], al[m][i]);
-              }
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int o = k + tid4 + 4 * i;
-                cut_tf32(x0[o * kXhStride + 16 * c + 8 * j + gid], bh[j][i], bl[j][i]);
-              }
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                mma_tf32(acc[m][j], al[m], bh[j]);
-                mma_tf32(acc[m][j], ah[m], bl[j]);
-                mma_tf32(acc[m][j], ah[m], bh[j]);
-              }
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                ub[(2 * tid4 + (i & 1)) * kUStride + 16 * m + gid + 8 * (i >> 1)] = acc[m][j][i];
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              F[8 * c + 4 * j + i] =
-                  add2(F[8 * c + 4 * j + i], pack2(ub[2 * i * kUStride + lane], ub[(2 * i + 1) * kUStride + lane]));
-            __syncwarp();
-          }
-        }
-      };
-      if (n_out > 0) add_channels(min(n_out, kOutHeld));
-      // channels past the held ones: kOutHeld at a time into the same place
-      for (int o0 = kOutHeld; o0 < n_out; o0 += kOutHeld) {
-        const int no = min(kOutHeld, n_out - o0);
-        ok = out_sync();  // the channels before are used
-        if (!ok) break;
-        const int k = (int)threadIdx.x - 128 - 32 * kOperandWarps;
-        static_assert(kPromoteThreads == 2 * kRows && kPromoteThreads >= kTokens, "two rows of weights a pass, a token per thread");
-        const int no8 = (no + 7) & ~7;  // (zero up to the next eight)
-#pragma unroll 8
-        for (int o = 0; o < no8; ++o)
-          if (k < kTokens)
-            xh_all[(1 + o) * kXhStride + k] = o < no && k < t.cnt ? __ldg(p.xop + (int64_t)(o0 + o) * a.n + t.p0 + k) : 0.0f;
-#pragma unroll 8
-        for (int o = k / kRows; o < no8; o += 2)
-          wh_all[o * kWhStride + k % kRows] = o < no ? wout[(o0 + o) * kRows + k % kRows] : 0.0f;
-        ok = out_sync();
-        if (!ok) break;
-        add_channels(no);
-      }
-      if (!ok) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&aux->wo_empty);
+      for (int kb = a.tpr; kb < steps; ++kb, ++g) {  // the outlier chunks
+        const int b = (int)(g & 1u);
+        ok = warp_wait(&aux->accf[b], (g >> 1) & 1u, aux, p);
+        if (!ok) break;
+        fence_after();
+        tmem_pieces(tmem + ((uint32_t)(32 * q) << 16) + kTokens + kTokens * b + t0, cols, [&](int c, const int(&r)[16]) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            F[8 * c + i] = add2(F[8 * c + i], pack2(__int_as_float(r[2 * i]), __int_as_float(r[2 * i + 1])));
+        });
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&aux->acce[b]);
+      }
+      if (!ok) break;
       if (live) {
         float* yr = a.y + (int64_t)(t.p0 + t0) * a.N + row;
 #pragma unroll
@@ -732,7 +703,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Before the tiles: each place's activation codes (GATHER: rows in place order for
-// the TMA), scale and outlier values, one warp per place.
+// the TMA), scale and outlier values (rows of a chunk's 16 channels,
+// cut in two), one warp per place.
 template <bool GATHER>
 __global__ void __launch_bounds__(256) k_grouped_rows(const GroupedArgs a, int8_t* xs, float* sxp, float* xop) {
   const int lane = threadIdx.x & 31;
@@ -755,7 +727,10 @@ __global__ void __launch_bounds__(256) k_grouped_rows(const GroupedArgs a, int8_
       for (int i = lane; i < a.xs / 16; i += 32) dst[i] = __ldg(src + i);
     }
     if (lane == 0) sxp[p] = __ldg(a.sx + r);
-    for (int i = lane; i < a.n_out; i += 32) xop[(int64_t)i * a.n + p] = __ldg(a.xout + (int64_t)r * a.n_out + i);
+    for (int i = lane; i < (a.n_out + kOutChunk - 1) / kOutChunk * kOutChunk; i += 32) {
+      float* dst = xop + ((int64_t)(i / kOutChunk) * a.n + p) * (2 * kOutChunk) + i % kOutChunk;
+      cut_tf32(i < a.n_out ? __ldg(a.xout + (int64_t)r * a.n_out + i) : 0.0f, dst[0], dst[kOutChunk]);
+    }
   }
 }
 
@@ -772,19 +747,18 @@ Carve carve(int K, int64_t n, int sm_count) {
   };
   c.xs = take((size_t)n * xq_stride_of(K));
   c.sxp = take((size_t)n * 4);
-  c.xop = take((size_t)n * kMaxOut * 4);
-  c.wout = take((size_t)sm_count * 2 * kMaxOut * kRows * 4);
+  c.xop = take((size_t)n * kMaxOut * 8);
+  c.wout = take((size_t)sm_count * kMaxOut * kRows * 4);
   c.total = off;
   return c;
 }
 
 template <bool MASK>
-cudaError_t launch_tiles(const CUtensorMap& mb, const WeightMaps& wm, Params p, int grid, cudaStream_t stream) {
+cudaError_t launch_tiles(const CUtensorMap& mb, const CUtensorMap& mx, const WeightMaps& wm, Params p, int grid, cudaStream_t stream) {
   p.off_raw = kStages * kStageBytes;
-  p.off_xh = p.off_raw + Raw<MASK>::kStages * Raw<MASK>::kBytes;
-  p.off_wh = p.off_xh + (1 + kOutHeld) * kXhStride * 4;
-  p.off_u = p.off_wh + kOutHeld * kWhStride * 4;
-  p.off_aux = p.off_u + kPromoteThreads / 32 * 8 * kUStride * 4;
+  p.off_sx = p.off_raw + Raw<MASK>::kStages * Raw<MASK>::kBytes;
+  p.off_wh = p.off_sx + kTokens * 4;
+  p.off_aux = p.off_wh + kOutHeld * kRows * 4;
   p.off_pre = p.off_aux + (int)round_up(sizeof(Aux), 16);
   p.off_ostart = p.off_pre + (int)round_up(4 * (p.a.E + 1), 16);
   p.off_oj = p.off_ostart + 4 * (p.a.tpr + 1);
@@ -810,7 +784,7 @@ cudaError_t launch_tiles(const CUtensorMap& mb, const WeightMaps& wm, Params p, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, mb, wm, p);
+  return cudaLaunchKernelEx(&cfg, fn, mb, mx, wm, p);
 }
 
 }  // namespace
@@ -830,7 +804,6 @@ cudaError_t launch_grouped_tc5(const GroupedArgs& a, void* workspace, int sm_cou
   float* sxp = reinterpret_cast<float*>(w + c.sxp);
   float* xop = reinterpret_cast<float*>(w + c.xop);
   p.sxp = sxp;
-  p.xop = xop;
   p.wout = reinterpret_cast<float*>(w + c.wout);
   p.rt = (int)ceil_div(a.rbe, kBlocks);
   // rows of the activation map: the places (in place order already without an
@@ -839,6 +812,11 @@ cudaError_t launch_grouped_tc5(const GroupedArgs& a, void* workspace, int sm_cou
   const int64_t rows = a.order ? a.n : std::min(a.n, a.rows);
   if (!tc05::make_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.order ? xs : a.xq, (uint64_t)a.xs, (uint64_t)rows,
                       (uint64_t)a.xs, kTileK, kTokenUnit, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  CUtensorMap mx;  // rows of the outlier chunks
+  if (!tc05::make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, xop, 8 * kOutChunk,
+                      (uint64_t)a.n * std::max<int64_t>(1, ceil_div(a.n_out, kOutChunk)), 8 * kOutChunk, 8 * kOutChunk,
+                      kTokenUnit, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   WeightMaps wm;
   const uint64_t blocks = (uint64_t)a.E * a.rbe;
@@ -864,7 +842,7 @@ cudaError_t launch_grouped_tc5(const GroupedArgs& a, void* workspace, int sm_cou
   const int64_t tiles = std::min<int64_t>(a.n, a.E + a.n / kTokens) * p.rt;
   if (tiles >= INT32_MAX) return cudaErrorInvalidValue;
   const int grid = (int)std::min<int64_t>(tiles, sm_count);
-  return a.mask ? launch_tiles<true>(mb, wm, p, grid, stream) : launch_tiles<false>(mb, wm, p, grid, stream);
+  return a.mask ? launch_tiles<true>(mb, mx, wm, p, grid, stream) : launch_tiles<false>(mb, mx, wm, p, grid, stream);
 }
 
 }  // namespace sq
