@@ -503,9 +503,10 @@ cudaError_t launch_kind(const GroupedArgs& a, int sm_count, cudaStream_t stream)
 
 }  // namespace
 
-// Measured crossover (8 experts 4096 x 4096: 51 us at 16, 80 us at 32 places per expert with the
-// few-token kernel, 75 and 81 us with the other; 4 experts 4096 -> 14336: 87 and 141, 137 and 141).
-bool grouped_many(int E, int64_t n) { return n >= 32 * (int64_t)E; }
+// Measured crossover, few-token kernel against the other, us at 16, 24 and 32 places per
+// expert: 8 experts 4096 x 4096 54 : 63, 63 : 64, 92 : 64; 32 experts 2048 -> 1408 46 : 59,
+// 64 : 60, 79 : 61; 4 experts 4096 -> 14336 93 : 117, 125 : 118, 138 : 118.
+bool grouped_many(int E, int64_t n) { return n >= 24 * (int64_t)E; }
 
 size_t grouped_workspace_bytes(int E, int K, int64_t n, bool asym, int sm_count) {
   return grouped_many(E, n) && !asym ? grouped_tc5_workspace_bytes(K, n, sm_count) : 0;
