@@ -198,15 +198,21 @@ struct Raw8 {
   }
 };
 // Elements i0 .. i0 + 7 of row `row` of a matrix of rows `ld` apart, `len` long; zero
-// unless `live`.  base points at a readable row in any case.
+// unless `live`.  base points at a readable row in any case.  In two halves, so that
+// a load can be issued long before its use.
+template <bool VEC, class T>
+__device__ __forceinline__ void issue_masked(Raw8<T>& r, const T* row, int i0, int len, bool live) {
+  if constexpr (VEC) r.load(row + (i0 < len ? i0 : 0));  // a vector lies inside the row or outside it, or crosses `len`
+  else r.gather(row, i0, live ? len : 0);
+}
+template <bool VEC, class T>
+__device__ __forceinline__ void finish_masked(Raw8<T>& r, int i0, int len, bool live) {
+  if constexpr (VEC) r.keep(live ? len - i0 : 0);
+}
 template <bool VEC, class T>
 __device__ __forceinline__ void load_masked(Raw8<T>& r, const T* row, int i0, int len, bool live) {
-  if constexpr (VEC) {  // a vector lies inside the row or outside it, or crosses `len`
-    r.load(row + (i0 < len ? i0 : 0));
-    r.keep(live ? len - i0 : 0);
-  } else {
-    r.gather(row, i0, live ? len : 0);
-  }
+  issue_masked<VEC>(r, row, i0, len, live);
+  finish_masked<VEC>(r, i0, len, live);
 }
 
 // The MMA's k index is free as long as both operands agree: over 32 channels lane
@@ -464,18 +470,25 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) k_lora_decode(const Params 
 
 // ---- many tokens ------------------------------------------------------------------------
 // Shrink: a cluster (of one CTA where there are tokens enough) takes 16 tokens of one
-// adapter, its warps split the channels; the parts meet in shared memory, then
-// over the cluster, and are summed in a fixed order.
-constexpr int kShrinkThreads = 512;
+// adapter; a warp has 32 of the rank and a slice of the channels (of 16 warps, Rp / 32
+// share a slice, so that its x comes from the first-level cache).  The next step's x
+// and weights are loaded as soon as this step's have left their registers.  The
+// parts meet in shared memory, then over the cluster, and are summed in a fixed
+// order.  What bounds it is the latency of those loads: with 64 of the rank per warp
+// the accumulators and parts spilled, and 2048 tokens, rank 64, 4096 -> 14336 took
+// 104 us against 95 (both kernels).
+constexpr int kShrinkThreads = 512, kShrinkWarps = kShrinkThreads / 32;
 constexpr int kGroupTokens = 16;
 
-template <class W, bool VEC, int NT>
+template <class W, bool VEC>
 __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) {
-  extern __shared__ __align__(16) float sm[];  // [warps][16][Rp], then the tile sums [S + 1]
+  extern __shared__ __align__(16) float sm[];  // [slices][16][Rp], then the tile sums [S + 1]
   __shared__ int part_i[kShrinkThreads / 32];
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = p.cluster, c = (int)cluster.block_rank(), u = blockIdx.y;
-  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tid4 = lane & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tid4 = lane & 3;
+  const int rgroups = p.Rp / 32, warps = kShrinkWarps / rgroups;  // slices of the channels in this CTA
+  const int part = warp / rgroups, r0 = 32 * (warp % rgroups);    // this warp's (a warp past them idles)
   int* pre = reinterpret_cast<int*>(sm + warps * kGroupTokens * p.Rp);
   pdl_wait();
   pdl_launch_dependents();
@@ -485,10 +498,10 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) 
   const int2 seg = segment_bounds(p.offsets, p.M, a, p.status);
   const int p0 = seg.x + (u - pre[a]) * kGroupTokens, cnt = min(kGroupTokens, seg.y - p0);
   const int rank = adapter_rank(p, a);
-  const int steps = (p.K + 31) / 32, slice = c * warps + warp, slices = nc * warps;
+  const int steps = (p.K + 31) / 32, slice = c * warps + part, slices = nc * warps;
   const int s0 = (int)((int64_t)steps * slice / slices), s1 = (int)((int64_t)steps * (slice + 1) / slices);
-  float* mine = sm + warp * kGroupTokens * p.Rp;
-  {
+  float* mine = sm + part * kGroupTokens * p.Rp;
+  if (part < warps) {
     const float* xr[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -500,79 +513,96 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) 
       xr[h] = p.x + (int64_t)t * p.K;
     }
     const W* Aa = static_cast<const W*>(p.A) + (int64_t)a * p.R * p.K;
-    for (int r0 = 0; r0 < p.Rp; r0 += 8 * NT) {  // (one pass up to rank 8 NT)
-      // the products of leading parts, and the rest: an addition of the tensor cores
-      // may truncate, so the many small ones are kept from the large sum
-      constexpr bool SPLIT = Parts<W>::n > 1;
-      float acc[NT][4] = {}, low[SPLIT ? NT : 1][4] = {};
-      if (r0 < rank) {
-        for (int s = s0; s < s1; ++s) {
-          const int k = 32 * s + 8 * tid4;
-          Raw8<float> xr8[2];
+    // the products of leading parts, and the rest: an addition of the tensor cores
+    // may truncate, so the many small ones are kept from the large sum
+    constexpr bool SPLIT = Parts<W>::n > 1;
+    constexpr int NT = 4;
+    float acc[NT][4] = {}, low[SPLIT ? NT : 1][4] = {};
+    if (r0 < rank && s0 < s1) {
+      Raw8<float> xr8[2];
+      Raw8<W> wr8[NT];
+      int wrow[NT];  // (R K < 2^25)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) load_masked<VEC>(xr8[h], xr[h], k, p.K, true);
-          Raw8<W> wr8[NT];
+      for (int j = 0; j < NT; ++j) wrow[j] = min(r0 + 8 * j + gid, rank - 1) * p.K;
+      auto issue_x = [&](int k) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) issue_masked<VEC>(xr8[h], xr[h], k, p.K, true);
+      };
+      auto issue_w = [&](int j, int k) { issue_masked<VEC>(wr8[j], Aa + wrow[j], k, p.K, r0 + 8 * j + gid < rank); };
+      constexpr bool AHEAD = sizeof(W) == 2;  // (no registers for it with binary32 weights)
+      issue_x(32 * s0 + 8 * tid4);
+      if constexpr (AHEAD) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) issue_w(j, 32 * s0 + 8 * tid4);
+      }
+      for (int s = s0; s < s1; ++s) {
+        const int k = 32 * s + 8 * tid4, next = min(s + 1, s1 - 1) * 32 + 8 * tid4;
+        if constexpr (!AHEAD) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j) issue_w(j, k);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) finish_masked<VEC>(xr8[h], k, p.K, true);
+        if constexpr (Parts<W>::n == 1) {
+          uint32_t xa[2][3][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) xr8[h].parts(xa[h]);
+          issue_x(next);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            const int r = r0 + 8 * j + gid;
-            load_masked<VEC>(wr8[j], Aa + (int64_t)min(r, rank - 1) * p.K, k, p.K, r < rank);
-          }
-          if constexpr (Parts<W>::n == 1) {
-            uint32_t xa[2][3][4];
+            if (r0 + 8 * j >= rank) break;
+            finish_masked<VEC>(wr8[j], k, p.K, r0 + 8 * j + gid < rank);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) xr8[h].parts(xa[h]);
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              if (r0 + 8 * j >= rank) break;
-#pragma unroll
-              for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int i = 2; i >= 0; --i) {  // small products first
-                  const uint32_t av[4] = {xa[0][i][2 * q], xa[1][i][2 * q], xa[0][i][2 * q + 1], xa[1][i][2 * q + 1]};
-                  mma_bf16(acc[j], av, wr8[j].w[2 * q], wr8[j].w[2 * q + 1]);
-                }
-            }
-          } else {
-            // k8 step q: channels 2q, 2q + 1 of the lane's eight
-            uint32_t xh[2][8], xl[2][8];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) cut_tf32(__uint_as_float(xr8[h].w[i]), xh[h][i], xl[h][i]);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              if (r0 + 8 * j >= rank) break;
-              float wv[8];
-              wr8[j].floats(wv);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                uint32_t h0 = __float_as_uint(wv[2 * q]), h1 = __float_as_uint(wv[2 * q + 1]);
-                if constexpr (Parts<W>::n == 3) {
-                  uint32_t l0, l1;
-                  cut_tf32(wv[2 * q], h0, l0);
-                  cut_tf32(wv[2 * q + 1], h1, l1);
-                  mma_tf32(low[SPLIT ? j : 0], xh[0][2 * q], xh[1][2 * q], xh[0][2 * q + 1], xh[1][2 * q + 1], l0, l1);
-                }
-                mma_tf32(low[SPLIT ? j : 0], xl[0][2 * q], xl[1][2 * q], xl[0][2 * q + 1], xl[1][2 * q + 1], h0, h1);
-                mma_tf32(acc[j], xh[0][2 * q], xh[1][2 * q], xh[0][2 * q + 1], xh[1][2 * q + 1], h0, h1);
+              for (int i = 2; i >= 0; --i) {  // small products first
+                const uint32_t av[4] = {xa[0][i][2 * q], xa[1][i][2 * q], xa[0][i][2 * q + 1], xa[1][i][2 * q + 1]};
+                mma_bf16(acc[j], av, wr8[j].w[2 * q], wr8[j].w[2 * q + 1]);
               }
+            issue_w(j, next);
+          }
+        } else {
+          // k8 step q: channels 2q, 2q + 1 of the lane's eight
+          uint32_t xh[2][8], xl[2][8];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) cut_tf32(__uint_as_float(xr8[h].w[i]), xh[h][i], xl[h][i]);
+          issue_x(next);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if (r0 + 8 * j >= rank) break;
+            finish_masked<VEC>(wr8[j], k, p.K, r0 + 8 * j + gid < rank);
+            float wv[8];
+            wr8[j].floats(wv);
+            if constexpr (AHEAD) issue_w(j, next);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t h0 = __float_as_uint(wv[2 * q]), h1 = __float_as_uint(wv[2 * q + 1]);
+              if constexpr (Parts<W>::n == 3) {
+                uint32_t l0, l1;
+                cut_tf32(wv[2 * q], h0, l0);
+                cut_tf32(wv[2 * q + 1], h1, l1);
+                mma_tf32(low[SPLIT ? j : 0], xh[0][2 * q], xh[1][2 * q], xh[0][2 * q + 1], xh[1][2 * q + 1], l0, l1);
+              }
+              mma_tf32(low[SPLIT ? j : 0], xl[0][2 * q], xl[1][2 * q], xl[0][2 * q + 1], xl[1][2 * q + 1], h0, h1);
+              mma_tf32(acc[j], xh[0][2 * q], xh[1][2 * q], xh[0][2 * q + 1], xh[1][2 * q + 1], h0, h1);
             }
           }
         }
       }
-      if constexpr (SPLIT) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[j][i] += low[j][i];
-      }
+    }
+    if constexpr (SPLIT) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        if (r0 + 8 * j < p.Rp) {
-          float* o = mine + gid * p.Rp + r0 + 8 * j + 2 * tid4;
-          *reinterpret_cast<float2*>(o) = make_float2(acc[j][0], acc[j][1]);
-          *reinterpret_cast<float2*>(o + 8 * p.Rp) = make_float2(acc[j][2], acc[j][3]);
-        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] += low[j][i];
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      float* o = mine + gid * p.Rp + r0 + 8 * j + 2 * tid4;
+      *reinterpret_cast<float2*>(o) = make_float2(acc[j][0], acc[j][1]);
+      *reinterpret_cast<float2*>(o + 8 * p.Rp) = make_float2(acc[j][2], acc[j][3]);
     }
   }
   __syncthreads();
@@ -941,12 +971,10 @@ cudaError_t launch_type(Params p, void* sort_ws, int32_t* sort_arrays, int sm_co
     const int64_t units = ceil_div(p.M, kGroupTokens);
     p.cluster = 1;
     while (p.cluster < kCluster && units * p.cluster * 2 <= sm_count) p.cluster *= 2;
-    const int threads = p.Rp <= 192 ? kShrinkThreads : kShrinkThreads / 2;  // (16 warps' parts must fit)
-    const int smem = threads / 32 * kGroupTokens * p.Rp * 4 + tables;
-    auto* fn = p.Rp <= 32 ? (veck ? k_lora_shrink<W, true, 4> : k_lora_shrink<W, false, 4>)
-                          : (veck ? k_lora_shrink<W, true, 8> : k_lora_shrink<W, false, 8>);
+    const int smem = kShrinkWarps / (p.Rp / 32) * kGroupTokens * p.Rp * 4 + tables;
+    auto* fn = veck ? k_lora_shrink<W, true> : k_lora_shrink<W, false>;
     const int groups = (int)(p.M / kGroupTokens + std::min(p.S, p.M));
-    const cudaError_t e = launch(fn, dim3(p.cluster, groups), threads, smem, p.cluster, true, stream, p);
+    const cudaError_t e = launch(fn, dim3(p.cluster, groups), kShrinkThreads, smem, p.cluster, true, stream, p);
     if (e != cudaSuccess) return e;
   }
   // columns per CTA: a few CTAs per SM over all tiles
