@@ -247,3 +247,115 @@ def test_a_layer_of_experts_end_to_end():
             want[t] += gates[t, j] * ref
             mag[t] += gates[t, j] * oracle.abs_dot(W2[ids[t, j]], hp)[0]
     assert (np.abs(out.cpu().numpy() - want) <= 2 * TOL * mag).all()
+
+
+# ---- many tokens per expert (the tcgen05 kernel: 24 entries per expert and more) -----
+# Outlier products there are sums of tf32 parts that miss 2^-21 of each product and may
+# truncate 2^-23 of a sum of 24 terms per addition: 2e-6 of the sum of magnitudes, within TOL.
+@pytest.mark.parametrize("P", [-1, 60])
+@pytest.mark.parametrize("n_out", [1, 15, 16, 17, 33, 100, 128, 129])
+def test_outlier_chunks_with_many_tokens(n_out, P):
+    c = Case(3, 200, 1000, [170, 0, 33], P=P, n_out=n_out)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("N,K,counts,div", [
+    (1, 1, [321], 1), (17, 128, [161, 1, 480], 3), (129, 129, [31, 33, 160, 0], 5), (300, 384, [1, 700, 0, 0, 2], 7),
+    (4090, 256, [100, 3], 2)])
+def test_tiles_of_many_tokens(N, K, counts, div):
+    """Tokens just around a tile's 160, one channel group per tile, rows past a tile's 128."""
+    c = Case(len(counts), N, K, counts, n_out=min(K, 3), div=div, spare=2)
+    c.check(c.run())
+
+
+def test_outliers_crowded_into_one_group_with_many_tokens():
+    c = Case(2, 260, 512, [60, 170], n_out=40)
+    c.idx = np.arange(250, 290, dtype=np.int32)
+    c.idxd = torch.from_numpy(c.idx).cuda()
+    c.xq, c.sx, c.xo = sq.quantize_act(torch.from_numpy(c.x).cuda(), c.idxd)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("E,per", [(33, 1), (40, 30), (1024, 1), (1024, 25)])
+def test_many_experts(E, per):
+    """More experts than a warp's lanes, up to the largest stack, in both kernels."""
+    rng = np.random.default_rng(E + per)
+    counts = rng.multinomial(E * per, rng.dirichlet(np.full(E, 0.3))).tolist()
+    c = Case(E, 24, 200, counts, n_out=2, spare=1)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("per", [2, 60])
+def test_an_entry_that_occurs_twice(per):
+    c = Case(3, 100, 300, [per, per, per])
+    order = c.order.copy()
+    order[per:2 * per] = order[:per]  # the same rows at two experts
+    order[1] = order[0]               # and twice at one
+    c.src = order // c.div
+    c.ordd.copy_(torch.from_numpy(order))
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("counts", [[2, 3], [60, 70]])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_row_that_is_not_finite_touches_no_other(counts, value):
+    c = Case(2, 150, 400, counts, n_out=3, div=1)
+    y = c.run()
+    c.check(y)
+    row = int(c.src[1])
+    x = torch.from_numpy(c.x).cuda()
+    x[row, 5] = value
+    x[row, int(c.idx[0])] = value
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.xq, c.sx, c.xo = sq.quantize_act(x, c.idxd, status=st)
+    z = c.run()
+    other = torch.arange(c.n, device="cuda") != 1
+    assert torch.equal(y[other], z[other])
+
+
+@pytest.mark.parametrize("what", ["descending", "past_n", "negative", "order", "order_negative", "idx", "idx_past_k"])
+def test_bad_device_arrays_are_reported_with_many_tokens(what):
+    c = Case(3, 140, 256, [40, 170, 30])
+    n = c.n
+    torch.cuda.synchronize()
+    if what == "descending":
+        c.offd.copy_(torch.tensor([0, 200, 40, n]))
+    elif what == "past_n":
+        c.offd.copy_(torch.tensor([0, 40, 210, 1 << 30]))
+    elif what == "negative":
+        c.offd.copy_(torch.tensor([-5, 40, 210, n]))
+    elif what == "order":
+        c.ordd[3] = c.rows * c.div
+    elif what == "order_negative":
+        c.ordd[3] = -1
+    elif what == "idx":
+        c.idxd.copy_(torch.tensor([1, 5, 5, 9, 200]))
+    else:
+        c.idxd.copy_(torch.tensor([1, 5, 6, 9, 256]))
+    c.run()
+    torch.cuda.synchronize()
+    assert c.status.item() == sq.STATUS_CODE["SQ_ERR_INVALID_ARG"]
+
+
+def test_a_captured_call_with_many_tokens_follows_the_route():
+    """Captured once with its workspace, beside eager calls between the replays."""
+    c = Case(3, 96, 384, [100, 0, 7], spare=60, n_out=20)
+    ws = sq.new_grouped_workspace(c.experts, c.n)
+    c.run(workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = c.run(workspace=ws, pdl=True)
+    rng = np.random.default_rng(6)
+    for counts in ([100, 0, 7], [0, 167, 0], [1, 1, 1], [0, 0, 0], [50, 50, 67]):
+        c.offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        order = rng.permutation(c.rows * c.div)[:c.n].astype(np.int32)
+        order[c.offsets[-1]:] = -1
+        c.src = order // c.div
+        c.offd.copy_(torch.from_numpy(c.offsets))
+        c.ordd.copy_(torch.from_numpy(order))
+        y.fill_(12345.0)
+        torch.cuda.synchronize()
+        g.replay()
+        c.check(y)
+        c.check(c.run())
