@@ -753,7 +753,7 @@ sq_status sq_grouped_linear(const sq_packed_weight* stack, int32_t E, int32_t N,
 sq_status sq_combine(const float* z, int32_t rows, const float* gates, const int32_t* place, int32_t T, int32_t k,
                      int32_t N, const float* base, float* out, int32_t* dev_status, uint32_t flags, void* stream) {
   if (!z || !gates || !place || !out) return SQ_ERR_INVALID_ARG;
-  if (T < 1 || k < 1 || k > kMaxChoices || (int64_t)T * k > kMaxEntries || N < 1 || N > (1 << 24) || rows < 1 ||
+  if (T < 1 || k < 1 || k > kMaxChoices || (int64_t)T * k > kMaxEntries || N < 1 || N > 65535 * 256 || rows < 1 ||
       rows > kMaxEntries)
     return SQ_ERR_SHAPE;
   if (flags & ~SQ_LAUNCH_PDL) return SQ_ERR_INVALID_ARG;

@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) 
   extern __shared__ __align__(16) float sm[];  // [slices][16][Rp], then the tile sums [S + 1]
   __shared__ int part_i[kShrinkThreads / 32];
   cg::cluster_group cluster = cg::this_cluster();
-  const int nc = p.cluster, c = (int)cluster.block_rank(), u = blockIdx.y;
+  const int nc = p.cluster, c = (int)cluster.block_rank(), u = (int)blockIdx.x / nc;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tid4 = lane & 3;
   const int rgroups = p.Rp / 32, warps = kShrinkWarps / rgroups;  // slices of the channels in this CTA
   const int part = warp / rgroups, r0 = 32 * (warp % rgroups);    // this warp's (a warp past them idles)
@@ -974,7 +974,7 @@ cudaError_t launch_type(Params p, void* sort_ws, int32_t* sort_arrays, int sm_co
     const int smem = kShrinkWarps / (p.Rp / 32) * kGroupTokens * p.Rp * 4 + tables;
     auto* fn = veck ? k_lora_shrink<W, true> : k_lora_shrink<W, false>;
     const int groups = (int)(p.M / kGroupTokens + std::min(p.S, p.M));
-    const cudaError_t e = launch(fn, dim3(p.cluster, groups), kShrinkThreads, smem, p.cluster, true, stream, p);
+    const cudaError_t e = launch(fn, dim3(p.cluster * groups), kShrinkThreads, smem, p.cluster, true, stream, p);
     if (e != cudaSuccess) return e;
   }
   // columns per CTA: a few CTAs per SM over all tiles

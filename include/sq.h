@@ -576,7 +576,8 @@ sq_status sq_grouped_linear(const sq_packed_weight *stack, int32_t E, int32_t N,
  *          SQ_ERR_INVALID_ARG)
  *   base   [T][N] f32, or NULL (then 0); may be out itself
  *   out    [T][N] f32; may not overlap z
- * Binary32 sums over j in ascending order.  1 <= k <= 32.  flags: SQ_LAUNCH_PDL.
+ * Binary32 sums over j in ascending order.  1 <= k <= 32, T*k and rows <= 2^24,
+ * N <= 65535*256.  flags: SQ_LAUNCH_PDL.
  */
 sq_status sq_combine(const float *z, int32_t rows, const float *gates, const int32_t *place,
                      int32_t T, int32_t k, int32_t N, const float *base, float *out,

@@ -236,3 +236,20 @@ def test_beside_the_shared_projection():
     c.base = ref
     want, tol = c.want()
     assert (np.abs(y.cpu().numpy() - want) <= tol + 1e-5 * oracle.abs_dot(W, c.x)).all()
+
+
+@pytest.mark.parametrize("M", [1 << 20, (1 << 20) - 7])
+def test_the_most_tokens(M):
+    """More 16-token groups than a grid has rows.  Small integers: every sum is exact."""
+    S, R, K, N = 3, 2, 8, 4
+    g = torch.Generator(device="cuda").manual_seed(M)
+    rnd = lambda *s: torch.randint(-3, 4, s, generator=g, device="cuda").float()
+    bank = sq.LoraBank(rnd(S, R, K), rnd(S, N, R), torch.tensor([1.0, 2.0, 0.5], device="cuda"))
+    x, base = rnd(M, K), rnd(M, N)
+    ids = torch.randint(-1, S, (M,), generator=g, device="cuda", dtype=torch.int32)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = sq.lora_add(bank, x, ids, base=base, status=st)
+    at = ids.clamp(min=0).long()
+    v = (bank.A[at] * x[:, None, :]).sum(2) * bank.scale[at][:, None]
+    want = base + torch.where(ids[:, None] >= 0, (bank.B[at] * v[:, None, :]).sum(2), 0.0)
+    assert st.item() == 0 and torch.equal(y, want)

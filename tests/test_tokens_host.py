@@ -139,3 +139,7 @@ def test_lora_refusals(L):
     assert L.sq_lora_workspace_bytes(ctypes.byref(bank()), 64) == 0
     need = L.sq_lora_workspace_bytes(ctypes.byref(bank()), 65)
     assert need >= 65 * 32 * 4 and call(M=65) == 8 and call(M=65, ws=P, wn=need - 1) == 8
+
+
+def test_combine_refuses_more_columns_than_a_grid_holds(L):
+    assert L.sq_combine(P, 8, P, P, 4, 2, 65535 * 256 + 1, None, P, None, 0, None) == 2
