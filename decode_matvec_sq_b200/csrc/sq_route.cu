@@ -4,15 +4,23 @@
 // tokens (sm_100a).
 //
 // Gate: per token the k largest logits, ties to the lower expert, by k rounds
-// of a warp-wide maximum (redux) over logits held in registers; softmax over
-// the chosen, or over all, experts with the row maximum subtracted.
+// of a warp-wide maximum (redux) over logits held in registers as ordered integers,
+// neighbouring experts in one lane, so that the first lane with the maximum is the
+// choice; softmax over the chosen, or over all, experts with the row maximum
+// subtracted.
 // Segments: a counting sort.  Every warp owns a contiguous span of a chunk of
 // entries; a lane's rank among equal ids of its 32 is a popcount of the
 // match mask, earlier batches and warps add their counts, so the order within a
 // segment is that of the entries whatever the timing (no atomic decides a
 // place).  Up to kSmallTokens tokens / one chunk of entries run in one CTA and
-// one launch (the latency of a decode step); more take two launches: counts
-// per chunk, then places.
+// one launch (the latency of a decode step: 4.1 us for 16 tokens of 64 experts,
+// k = 4); more take two launches: counts per chunk, then places, every CTA summing
+// the chunks' counts itself.
+// What bounds them: latency.  8192 tokens of 128 experts, k = 8, take 16.8 us
+// (10 MB in and out would be 1 us): two launches, in each a chain of load, sort
+// and store.  Experts spread over the lanes (lane + 32 i) took a second reduction
+// per choice, and the chunks' counts read after the chunk's own sort, 23.5 us.
+// Combine: one pass, bound by memory (4099 tokens, k = 4, 4096 columns: 6.3 TB/s).
 #include <stdint.h>
 
 #include <algorithm>
@@ -168,54 +176,67 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
 }
 __device__ __forceinline__ float exp_below(float v, float m) { return v == m ? 1.0f : expf(v - m); }
 
-// Routes token t by one warp; I logits per lane (expert lane + 32 i).  Lane j < k
-// returns the j-th choice (-1: fewer than k experts unmasked).
+__device__ __forceinline__ float key_logit(uint32_t key) {  // (of a key above kMasked)
+  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+
+// Routes token t by one warp; I neighbouring logits per lane (expert I lane + i, so
+// that among equal keys the first lane, and its first, is the lower expert).  Lane
+// j < k returns the j-th choice (-1: fewer than k experts unmasked).
 template <int I>
 __device__ int route_token(const RouteParams& p, int t) {
   const int lane = threadIdx.x & 31;
-  const float* l = p.logits + (int64_t)t * p.E;
+  const float* l = p.logits + (int64_t)t * p.E + I * lane;
   float v[I];
   uint32_t key[I];
   bool bad = false;
+  if (I >= 4 && (p.E & 3) == 0) {  // (rows are 16-byte aligned)
 #pragma unroll
-  for (int i = 0; i < I; ++i) {
-    const int e = lane + 32 * i;
-    v[i] = e < p.E ? __ldg(l + e) : -INFINITY;
+    for (int i = 0; i < I; i += 4) {
+      const float4 f = I * lane + i < p.E ? __ldg(reinterpret_cast<const float4*>(l + i))
+                                          : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      const float g[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+      for (int u = 0; u < 4 && i + u < I; ++u) v[i + u] = g[u];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < I; ++i) v[i] = I * lane + i < p.E ? __ldg(l + i) : -INFINITY;
   }
 #pragma unroll
   for (int i = 0; i < I; ++i) {
-    key[i] = lane + 32 * i < p.E ? logit_key(v[i]) : 0u;
+    key[i] = logit_key(v[i]);
     bad |= v[i] != v[i] || v[i] == INFINITY;
   }
   if (bad) set_status(p.status, SQ_ERR_NONFINITE);
   int id = -1;
-  float val = -INFINITY, top = 0.0f;
+  uint32_t chosen = 0u, first = 0u;
   for (int j = 0; j < p.k; ++j) {
-    uint32_t best = 0u;
-    int at = 0;
+    uint32_t best = key[0];
 #pragma unroll
-    for (int i = 0; i < I; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
-      }
+    for (int i = 1; i < I; ++i) best = max(best, key[i]);
     const uint32_t m = __reduce_max_sync(0xffffffffu, best);
     if (m <= kMasked) break;
-    const int e = (int)__reduce_min_sync(0xffffffffu, best == m ? (uint32_t)(lane + 32 * at) : 0xffffffffu);
-    float mine = 0.0f;
+    const int src = __ffs(__ballot_sync(0xffffffffu, best == m)) - 1;
+    int at = 0;
+    bool open = lane == src;
 #pragma unroll
-    for (int i = 0; i < I; ++i)
-      if (e == lane + 32 * i) {
-        mine = v[i];
+    for (int i = 0; i < I; ++i) {
+      const bool hit = open && key[i] == m;
+      if (hit) {
+        at = i;
         key[i] = 0u;
+        open = false;
       }
-    mine = __shfl_sync(0xffffffffu, mine, e & 31);
-    if (j == 0) top = mine;
+    }
+    const int e = I * src + __shfl_sync(0xffffffffu, at, src);
+    if (j == 0) first = m;
     if (lane == j) {
       id = e;
-      val = mine;
+      chosen = m;
     }
   }
+  const float top = key_logit(first), val = key_logit(chosen);
   float sum = 0.0f;
   if (p.all) {
 #pragma unroll
@@ -309,25 +330,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_place(const SegParams p) {
   pdl_wait();
   pdl_launch_dependents();
   const int e0 = blockIdx.x * p.chunk, n = min(p.chunk, p.n - e0);
-  load_ids(sm, p, e0, n);
-  __syncthreads();
-  count_chunk(sm, n, p.S);
-  // segment totals over all chunks, and over the chunks before this one
-  for (int s = threadIdx.x; s < p.S; s += kThreads) {
-    sm.total[s] = 0;
-    sm.base[s] = 0;
-  }
-  __syncthreads();
+  // segment totals over all chunks, and over the chunks before this one: loaded
+  // first, summed in shared memory when the chunk's own counts are done
   const int S32 = (p.S + 31) & ~31, groups = kThreads / S32;  // S <= 1024
   const int g = threadIdx.x / S32, s = threadIdx.x % S32;
+  int total = 0, before = 0;
   if (g < groups && s < p.S) {
-    int total = 0, before = 0;
 #pragma unroll 16
     for (int c = g; c < p.chunks; c += groups) {
       const int v = __ldg(p.counts + (int64_t)c * p.S + s);
       total += v;
       if (c < (int)blockIdx.x) before += v;
     }
+  }
+  load_ids(sm, p, e0, n);
+  __syncthreads();
+  count_chunk(sm, n, p.S);
+  for (int i = threadIdx.x; i < p.S; i += kThreads) {
+    sm.total[i] = 0;
+    sm.base[i] = 0;
+  }
+  __syncthreads();
+  if (g < groups && s < p.S) {
     atomicAdd(&sm.total[s], total);
     atomicAdd(&sm.base[s], before);
   }
