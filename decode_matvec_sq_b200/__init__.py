@@ -127,6 +127,8 @@ def lib():
         "sq_segment": ([vp, i32, i32, vp, vp, vp, vp, sz, vp, u32, vp], ctypes.c_int),
         "sq_expert_view": ([pw, i32, i32, i32, pw], ctypes.c_int),
         "sq_grouped_linear_workspace_bytes": ([pw, i32, i32, i32], sz),
+        "sq_testing_grouped_stalled": ([pw, i32, i32, vp, vp, vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, sz, i32,
+                                        ctypes.c_uint64, vp, vp], ctypes.c_int),
         "sq_grouped_linear": ([pw, i32, i32, vp, vp, vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, sz, vp, u32, vp],
                               ctypes.c_int),
         "sq_lora_workspace_bytes": ([lb, i32], sz),
@@ -796,6 +798,16 @@ def grouped_linear(experts: PackedExperts, xq, sx, x_out, idx, offsets, order=No
     if rc:
         _ck(rc, w)
     return y
+
+
+def testing_grouped_stalled(experts: PackedExperts, xq, sx, x_out, idx, offsets, order, div: int, y, workspace,
+                            skip_group: int, wait_ns: int, status=None, stream=None):
+    """include/sq_testing.h: sq_grouped_linear with one channel group never
+    requested and every wait limited to wait_ns (tests of the timeout path)."""
+    _ck(lib().sq_testing_grouped_stalled(
+        ctypes.byref(experts.view), experts.E, experts.N, _ptr(xq), _ptr(sx), _ptr(x_out), _ptr(idx), idx.numel(),
+        xq.shape[0], _ptr(order), div, _ptr(offsets), y.shape[0], _ptr(y), _ptr(workspace), workspace.numel(),
+        skip_group, wait_ns, _ptr(status), _stream(stream)), "sq_testing_grouped_stalled")
 
 
 def combine(z, gates, place, base=None, out=None, status=None, pdl: bool = False, stream=None):

@@ -702,10 +702,13 @@ size_t sq_grouped_linear_workspace_bytes(const sq_packed_weight* stack, int32_t 
   return grouped_workspace_bytes(E, stack->K, n, stack->layout == SQ_LAYOUT_TILES_ASYM, d.sm_count);
 }
 
-sq_status sq_grouped_linear(const sq_packed_weight* stack, int32_t E, int32_t N, const int8_t* xq, const float* sx,
-                            const float* x_out, const int32_t* idx, int32_t n_out, int32_t rows, const int32_t* order,
-                            int32_t div, const int32_t* offsets, int32_t n, float* y, void* workspace, size_t ws_bytes,
-                            int32_t* dev_status, uint32_t flags, void* stream) {
+static constexpr uint64_t kGroupedWaitNs = 1000000000ull;
+
+static sq_status grouped_linear(const sq_packed_weight* stack, int32_t E, int32_t N, const int8_t* xq, const float* sx,
+                                const float* x_out, const int32_t* idx, int32_t n_out, int32_t rows,
+                                const int32_t* order, int32_t div, const int32_t* offsets, int32_t n, float* y,
+                                void* workspace, size_t ws_bytes, int32_t* dev_status, uint32_t flags, void* stream,
+                                uint64_t wait_ns, int32_t skip_group) {
   sq_status st = check_stack(stack, E, N);
   if (st != SQ_OK) return st;
   if (!xq || !sx || !offsets || !y) return SQ_ERR_INVALID_ARG;
@@ -747,7 +750,17 @@ sq_status sq_grouped_linear(const sq_packed_weight* stack, int32_t E, int32_t N,
   a.y = y;
   a.status = dev_status;
   a.pdl = (flags & SQ_LAUNCH_PDL) ? 1 : 0;
+  a.wait_ns = wait_ns;
+  a.skip_group = skip_group;
   return from_cuda(launch_grouped(a, workspace, d.sm_count, static_cast<cudaStream_t>(stream)));
+}
+
+sq_status sq_grouped_linear(const sq_packed_weight* stack, int32_t E, int32_t N, const int8_t* xq, const float* sx,
+                            const float* x_out, const int32_t* idx, int32_t n_out, int32_t rows, const int32_t* order,
+                            int32_t div, const int32_t* offsets, int32_t n, float* y, void* workspace, size_t ws_bytes,
+                            int32_t* dev_status, uint32_t flags, void* stream) {
+  return grouped_linear(stack, E, N, xq, sx, x_out, idx, n_out, rows, order, div, offsets, n, y, workspace, ws_bytes,
+                        dev_status, flags, stream, kGroupedWaitNs, -1);
 }
 
 sq_status sq_combine(const float* z, int32_t rows, const float* gates, const int32_t* place, int32_t T, int32_t k,
@@ -851,6 +864,21 @@ extern "C" sq_status sq_testing_nvfp4_stalled(const sq_nvfp4_matrix* w, const sq
   if ((st = check_device(&d)) != SQ_OK) return st;
   return from_cuda(launch_nvfp4_gemm(*w, *x, y, dev_status, static_cast<cudaStream_t>(stream),
                                      wait_ns, skip_stage));
+}
+
+extern "C" sq_status sq_testing_grouped_stalled(const sq_packed_weight* stack, int32_t E, int32_t N, const int8_t* xq,
+                                                const float* sx, const float* x_out, const int32_t* idx,
+                                                int32_t n_out, int32_t rows, const int32_t* order, int32_t div,
+                                                const int32_t* offsets, int32_t n, float* y, void* workspace,
+                                                size_t ws_bytes, int32_t skip_group, uint64_t wait_ns,
+                                                int32_t* dev_status, void* stream) {
+  const sq_status st = check_stack(stack, E, N);
+  if (st != SQ_OK) return st;
+  if (!grouped_many(E, n) || !grouped_tc5_supported(n_out, stack->layout == SQ_LAYOUT_TILES_ASYM)) return SQ_ERR_SHAPE;
+  if (skip_group < -1 || skip_group >= (int32_t)ceil_div(stack->K, kTileK)) return SQ_ERR_INVALID_ARG;
+  if (wait_ns < 1 || wait_ns > 1000000000ull) return SQ_ERR_INVALID_ARG;
+  return grouped_linear(stack, E, N, xq, sx, x_out, idx, n_out, rows, order, div, offsets, n, y, workspace, ws_bytes,
+                        dev_status, 0, stream, wait_ns, skip_group);
 }
 
 extern "C" sq_status sq_testing_mma_peak(int32_t kind, int32_t iters, double* ops_per_s,

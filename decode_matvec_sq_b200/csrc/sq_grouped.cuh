@@ -34,6 +34,10 @@ struct GroupedArgs {
   float* y;
   int32_t* status;
   int pdl;
+  // for the tests (include/sq_testing.h): the limit of the many-token kernel's waits,
+  // and a channel group whose weights are never requested (-1: none)
+  uint64_t wait_ns;
+  int skip_group;
 };
 
 // a / b for 0 <= a, 0 < b, in 32 bits where a allows it (a 64-bit division costs

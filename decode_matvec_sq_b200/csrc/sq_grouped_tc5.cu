@@ -64,7 +64,7 @@ constexpr int kMaxOut = 128;        // outlier channels this kernel takes
 constexpr int kOutHeld = 32;        // of them held in shared memory under the tile's products
 constexpr int kOutChunk = 16;       // of them in one stage
 
-constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr uint64_t kWaitNs = 1000000000ull;  // of the waits when winding down
 
 template <bool MASK>
 struct Raw {
@@ -141,7 +141,7 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Au
     if ((n & 31u) == 31u) {
       const uint64_t now = global_ns();
       if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitNs) break;
+      if (now - t0 > p.a.wait_ns) break;
     }
   }
   set_status(p.a.status, SQ_ERR_TIMEOUT);
@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (g >= RW::kStages) ok = warp_wait(&aux->raw_empty[s], (use & 1u) ^ 1u, aux, p);
           ok = __all_sync(0xffffffffu, ok && !aborted(aux));
           if (!ok) break;
+          if (kb == a.skip_group) continue;
           uint8_t* st = smem + p.off_raw + s * RW::kBytes;
           // (row blocks past the expert are the next expert's, past the stack zero;
           // their rows are not written)

@@ -3,7 +3,7 @@
  * decode path; the pages have no counterpart to it.
  *
  * The prefill kernels -- sq_linear on many tokens (SQ_LAYOUT_ROWS, group size
- * 128) and sq_nvfp4_linear -- bound every wait on their pipeline barriers.  When a wait runs out, the
+ * 128), sq_nvfp4_linear and sq_grouped_linear on many tokens per expert -- bound every wait on their pipeline barriers.  When a wait runs out, the
  * kernel records SQ_ERR_TIMEOUT in the caller's status word and winds down:
  * it first waits (again bounded) for the operand copies it has requested and
  * for the tensor-core MMAs it has issued, then frees its tensor memory and
@@ -45,6 +45,23 @@ sq_status sq_testing_prefill_stalled(const sq_packed_weight *w, const int8_t *xq
 sq_status sq_testing_nvfp4_stalled(const sq_nvfp4_matrix *w, const sq_nvfp4_matrix *x, float *y,
                                    int32_t skip_stage, uint64_t wait_ns, int32_t *dev_status,
                                    void *stream);
+
+/*
+ * sq_grouped_linear on its many-token kernel (at least 24 places per expert, a
+ * symmetric residual, at most 128 outlier channels; else SQ_ERR_SHAPE) with its
+ * waits limited to wait_ns (1 .. 10^9 nanoseconds) and the weights of channel
+ * group skip_group (0 <= skip_group < ceil(K/128)) never requested for any tile;
+ * skip_group = -1 requests everything and gives the result of
+ * sq_grouped_linear.  The other arguments are those of sq_grouped_linear.  With a
+ * group skipped, dev_status ends up SQ_ERR_TIMEOUT and y is unspecified.
+ */
+sq_status sq_testing_grouped_stalled(const sq_packed_weight *stack, int32_t E, int32_t N,
+                                     const int8_t *xq, const float *sx, const float *x_out,
+                                     const int32_t *idx, int32_t n_out, int32_t rows,
+                                     const int32_t *order, int32_t div, const int32_t *offsets,
+                                     int32_t n, float *y, void *workspace, size_t ws_bytes,
+                                     int32_t skip_group, uint64_t wait_ns, int32_t *dev_status,
+                                     void *stream);
 
 /*
  * Dense tensor-core throughput probe, the peak the prefill kernels are

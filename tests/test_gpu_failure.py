@@ -136,3 +136,56 @@ def test_nvfp4_stalled_entry_rejects_bad_arguments():
         with pytest.raises(sq.SQError) as e:
             sq.testing_nvfp4_stalled(w, a, y, skip, wait)
         assert e.value.name == "SQ_ERR_INVALID_ARG"
+
+
+# ---- the linear layer grouped by expert, many tokens per expert ------------------------
+def _grouped_case(E, N, K, counts, n, seed):
+    rng = np.random.default_rng(seed)
+    W = rng.laplace(0, 0.02, (E, N, K)).astype(np.float32)
+    rows = int(sum(counts))
+    x = rng.standard_normal((rows, K)).astype(np.float32)
+    idx = np.sort(rng.choice(K, n, replace=False)).astype(np.int32)
+    x[:, idx] *= 30.0
+    experts = sq.alloc_experts(E, N, K)
+    for e in range(E):
+        sq.decompose_pack(torch.from_numpy(W[e]).cuda(), out=experts.expert(e))
+    idxd = torch.from_numpy(idx).cuda()
+    q = sq.quantize_act(torch.from_numpy(x).cuda(), idxd)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    order = torch.from_numpy(rng.permutation(rows).astype(np.int32)).cuda()
+    torch.cuda.synchronize()
+    return experts, q, idxd, off, order
+
+
+@pytest.mark.parametrize("N,K,counts,skip", [(200, 512, [70, 200], 1), (128, 128, [40], 0), (400, 1024, [1, 90, 170], 7),
+                                             (300, 2048, [330, 20], 9), (300, 512, [160, 160], -1)])
+def test_grouped_stalled_group_times_out_and_the_context_survives(N, K, counts, skip):
+    experts, q, idx, off, order = _grouped_case(len(counts), N, K, counts, 20, seed=N + K)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = sq.new_grouped_workspace(experts, sum(counts))
+    ref = sq.grouped_linear(experts, *q, idx, off, order=order, workspace=ws, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    y = torch.zeros_like(ref)
+    sq.testing_grouped_stalled(experts, *q, idx, off, order, 1, y, ws, skip, 1_000_000 if skip >= 0 else 1_000_000_000,
+                               status=st)
+    torch.cuda.synchronize()  # returns: the kernel wound down
+    if skip < 0:
+        assert st.item() == 0 and torch.equal(y, ref)
+        return
+    assert st.item() == sq.STATUS_CODE["SQ_ERR_TIMEOUT"]
+    # the same stream and workspace, the next call: runs and gives the same
+    st.zero_()
+    again = sq.grouped_linear(experts, *q, idx, off, order=order, workspace=ws, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0 and torch.equal(again, ref)
+
+
+def test_grouped_stalled_entry_rejects_bad_arguments():
+    experts, q, idx, off, order = _grouped_case(2, 64, 256, [30, 30], 3, seed=4)
+    ws, y = sq.new_grouped_workspace(experts, 60), torch.zeros(60, 64, device="cuda")
+    for skip, wait in [(2, 1000), (-2, 1000), (0, 0), (0, 2_000_000_000)]:
+        with pytest.raises(sq.SQError):
+            sq.testing_grouped_stalled(experts, *q, idx, off, order, 1, y, ws, skip, wait)
+    with pytest.raises(sq.SQError):  # too few places for that kernel
+        sq.testing_grouped_stalled(experts, *q, idx, off, order[:40].clone(), 1, y[:40], ws, -1, 1000)
