@@ -608,13 +608,20 @@ def _status_arg(status, dev: int, where: str):
     return _arg(status, torch.int32, (1,), dev, where, "status")
 
 
-def _stream_arg(stream, dev: int) -> int:
-    """The handle of a stream, or of the current stream of device `dev`."""
+def _stream_arg(dev: int) -> int:
+    """The handle of the current stream of device `dev`."""
     import torch
-    if stream is not None:
-        return stream.cuda_stream
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (the public call costs 3 us)
     return raw(dev) if raw else torch.cuda.current_stream().cuda_stream
+
+
+def _on(stream, call, *args):
+    """A call with `stream` as the current one, so that results and scratch come
+    from that stream's memory: what was freed on another may still be in use
+    there, and scratch is freed while the kernels of this one still use it."""
+    import torch
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
 def _workspace_arg(ws, need: int, device, dev: int, where: str):
@@ -647,6 +654,8 @@ def route(logits, k: int, gate: str = "topk", workspace=None, status=None, pdl: 
     """Top-k of logits [T][E] (float32) with softmax gates over the chosen
     ("topk") or over all experts ("all"), and the entries sorted by expert."""
     import torch
+    if stream is not None:
+        return _on(stream, route, logits, k, gate, workspace, status, pdl)
     if gate not in ("topk", "all"):
         _refuse("sq_route", 'gate must be "topk" or "all"')
     if logits.dim() != 2:
@@ -670,7 +679,7 @@ def route(logits, k: int, gate: str = "topk", workspace=None, status=None, pdl: 
     ws, wp, wn = _workspace_arg(workspace, L.sq_route_workspace_bytes(T, E, k), dev, cur, "sq_route")
     rc = L.sq_route(lp, T, E, k, SQ_GATE_ALL if gate == "all" else SQ_GATE_TOPK, ids.data_ptr(),
                     gates.data_ptr(), offsets.data_ptr(), order.data_ptr(), place.data_ptr(), wp, wn,
-                    _status_arg(status, cur, "sq_route"), _flags(pdl), _stream_arg(stream, cur))
+                    _status_arg(status, cur, "sq_route"), _flags(pdl), _stream_arg(cur))
     if rc:
         _ck(rc, "sq_route")
     return Route(offsets, order, place, ids, gates)
@@ -679,6 +688,8 @@ def route(logits, k: int, gate: str = "topk", workspace=None, status=None, pdl: 
 def segment(ids, S: int, workspace=None, status=None, pdl: bool = False, stream=None) -> Segments:
     """Entries with ids (int32, any shape, -1 = none) in [0, S) sorted by id."""
     import torch
+    if stream is not None:
+        return _on(stream, segment, ids, S, workspace, status, pdl)
     n = ids.numel()
     cur = torch.cuda.current_device() if ids.is_cuda else _NO_DEVICE
     ip = _arg(ids, torch.int32, ids.shape, cur, "sq_segment", "ids")
@@ -691,7 +702,7 @@ def segment(ids, S: int, workspace=None, status=None, pdl: bool = False, stream=
     L = lib()
     ws, wp, wn = _workspace_arg(workspace, L.sq_segment_workspace_bytes(n, S), dev, cur, "sq_segment")
     _ck(L.sq_segment(ip, n, S, offsets.data_ptr(), order.data_ptr(), place.data_ptr(), wp, wn,
-                     _status_arg(status, cur, "sq_segment"), _flags(pdl), _stream_arg(stream, cur)), "sq_segment")
+                     _status_arg(status, cur, "sq_segment"), _flags(pdl), _stream_arg(cur)), "sq_segment")
     return Segments(offsets, order, place)
 
 
@@ -772,6 +783,8 @@ def grouped_linear(experts: PackedExperts, xq, sx, x_out, idx, offsets, order=No
     activations (as from quantize_act) of row order[p] // div, or of row p
     without an order.  Rows from offsets[E] on are not written."""
     import torch
+    if stream is not None:
+        return _on(stream, grouped_linear, experts, xq, sx, x_out, idx, offsets, order, div, y, workspace, status, pdl)
     w = "sq_grouped_linear"
     E, N = experts.E, experts.N
     if xq.dim() != 2:
@@ -794,7 +807,7 @@ def grouped_linear(experts: PackedExperts, xq, sx, x_out, idx, offsets, order=No
     need = 0 if workspace is not None else grouped_workspace_bytes(experts, n)
     workspace, wp, wn = _workspace_arg(workspace, need, xq.device, cur, w)
     rc = L.sq_grouped_linear(ctypes.byref(experts.view), E, N, xp, sp, op, ip, nout, rows, dp, div, fp, n, yp, wp,
-                             wn, _status_arg(status, cur, w), _flags(pdl), _stream_arg(stream, cur))
+                             wn, _status_arg(status, cur, w), _flags(pdl), _stream_arg(cur))
     if rc:
         _ck(rc, w)
     return y
@@ -814,6 +827,8 @@ def combine(z, gates, place, base=None, out=None, status=None, pdl: bool = False
     """out [T][N] = base + sum_j gates[t][j] * z[place[t][j]] (float32); place -1
     adds nothing.  out may be base, not z."""
     import torch
+    if stream is not None:
+        return _on(stream, combine, z, gates, place, base, out, status, pdl)
     w = "sq_combine"
     if z.dim() != 2 or gates.dim() != 2:
         _refuse(w, "z must be [rows][N] and gates [T][k]", "SQ_ERR_SHAPE")
@@ -828,7 +843,7 @@ def combine(z, gates, place, base=None, out=None, status=None, pdl: bool = False
         out = torch.empty(T, N, dtype=f32, device=z.device)
     op = _arg(out, f32, (T, N), cur, w, "out")
     rc = lib().sq_combine(zp, rows, gp, pp, T, k, N, bp, op, _status_arg(status, cur, w), _flags(pdl),
-                          _stream_arg(stream, cur))
+                          _stream_arg(cur))
     if rc:
         _ck(rc, w)
     return out
@@ -888,6 +903,8 @@ def lora_add(bank: LoraBank, x, ids, base=None, y=None, segments: Segments = Non
     base and y may be column slices of wider matrices, and the same one (in
     place).  segments: segment(ids, bank.S), kept for the projections of a step."""
     import torch
+    if stream is not None:
+        return _on(stream, lora_add, bank, x, ids, base, y, segments, workspace, status, pdl)
     w = "sq_lora_add"
     if x.dim() != 2:
         _refuse(w, "x must be [M][K]", "SQ_ERR_SHAPE")
@@ -906,7 +923,7 @@ def lora_add(bank: LoraBank, x, ids, base=None, y=None, segments: Segments = Non
     need = 0 if workspace is not None else lora_workspace_bytes(bank, M)
     workspace, wp, wn = _workspace_arg(workspace, need, x.device, cur, w)
     rc = lib().sq_lora_add(ctypes.byref(bank.view), xp, M, ip, fp, op, bp, ldb, yp, ldy, wp, wn,
-                           _status_arg(status, cur, w), _flags(pdl), _stream_arg(stream, cur))
+                           _status_arg(status, cur, w), _flags(pdl), _stream_arg(cur))
     if rc:
         _ck(rc, w)
     return y
