@@ -792,6 +792,8 @@ def grouped_linear(experts: PackedExperts, xq, sx, x_out, idx, offsets, order=No
     f32, i32, cur = torch.float32, torch.int32, torch.cuda.current_device() if xq.is_cuda else _NO_DEVICE
     rows, nout = xq.shape[0], 0 if idx is None else idx.numel()
     xp = _arg(xq, torch.int8, (rows, experts.view.res_stride), cur, w, "xq")
+    if experts.keep[0].get_device() != cur:
+        _refuse(w, "the experts are not on the current device")
     sp = _arg(sx, f32, (rows,), cur, w, "sx")
     op = ip = None
     if nout:
@@ -911,6 +913,8 @@ def lora_add(bank: LoraBank, x, ids, base=None, y=None, segments: Segments = Non
     M, N = x.shape[0], bank.N
     cur = torch.cuda.current_device() if x.is_cuda else _NO_DEVICE
     xp = _arg(x, torch.float32, (M, bank.K), cur, w, "x")
+    if bank.A.get_device() != cur:
+        _refuse(w, "the adapters are not on the current device")
     ip = _arg(ids, torch.int32, (M,), cur, w, "ids")
     if y is None:
         y = torch.empty(M, N, dtype=torch.float32, device=x.device)

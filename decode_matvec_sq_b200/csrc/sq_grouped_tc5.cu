@@ -14,17 +14,25 @@
 //   warp 2: TMA of the group's activation codes (rows in place order);
 //   warps 4-11: turn the raw row blocks into the two K-major, 128-byte-swizzled
 //     int8 operands, codes and +-1 (0 outside the mask) trunk bytes;
-//   warp 3: the dequantized weights of the group's outlier channels;
+//   warp 3: picks the outlier channels' weights out of the raw row blocks as they
+//     pass and dequantizes them, and fetches the token scales;
 //   warp 1: per group, R into one of two tensor-memory buffers, and T;
 //   warps 12-19: read each group's R and add s_g R to binary32 registers; at the
-//     end of a tile read T, add the outlier channels and write y (warps 12-15 the
-//     first half of the tile's tokens, 16-19 the second).
-// What bounds it: the hand-overs.  With every copy, operand and promotion taken out
-// a group still costs 1400 clocks of barrier round trips in a chain of five roles
-// (16 MMAs a group on five barriers cost 2300; the eight here on two 1800 at 160
-// tokens, of which shared-memory traffic alone would be 1400).  Hence the wide
-// tile, one barrier per stage for both operands, and group scales that the
-// promotion reads from memory itself.
+//     end of a tile read T, apply alpha and sx, add the outlier chunks and write y
+//     (warps 12-15 the first half of the tile's tokens, 16-19 the second).
+// Outlier channels are further steps of the same pipeline, 16 a step: What and x_out
+// are cut into two tf32 parts each, and one stage holds [hi | hi] and [lo] of the
+// weights (written by warps 4-11) and [hi | lo] of the activations (cut by the
+// prologue kernel, brought by TMA); six kind::tf32 MMAs give all products but
+// lo x lo, below 2^-21 of the product.  20 outlier channels cost 8 % of the time (4096
+// places over 8 experts, 4096 -> 14336: 697 us without, 753 us with); on the CUDA
+// cores of the promotion, a row of weights per lane, they cost 30 %.
+// What bounds it: shared memory.  Raw tile in and out, both operands in and out,
+// activations in once and out twice are 160 KB a group, 1250 clocks; a group takes
+// 1300 clocks at 32 tokens (the hand-overs between five roles) and 1800 at 160.
+// Hence the wide tile, one barrier per stage for both operands, and group scales
+// that the promotion reads from memory itself.  At 753 us the whole call is 639
+// TFLOP/s of the layer's products, 0.39 of the measured bf16 rate.
 // The sums are integers because the tensor cores' binary32 sums are not exact
 // enough: 16-bit operands accumulated over K = 4096 measured 4.4e-6 relative
 // error (a truncation that grows with K; 1.6e-5 at 14336), the integer sums none.

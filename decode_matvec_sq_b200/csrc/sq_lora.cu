@@ -6,23 +6,31 @@
 // A_a [rank_a][K], B_a [N][rank_a] in binary32, binary16 or bfloat16, x, base and
 // y in binary32, every product and sum in binary32 or better.
 //
-// Few tokens (a decode step): one launch.  A cluster of kCluster CTAs serves up
+// Few tokens (a decode step): one launch.  A cluster of 8 or 16 CTAs serves up
 // to kGroup tokens that share an adapter (found from the ids by ballots): each CTA
-// forms its channels' part of v = A x on the CUDA cores, the parts meet over
-// distributed shared memory, and each CTA adds its columns of B v.  The adapter
-// is read once, by the cluster, and there is no second launch to wait for.
+// forms its channels' part of v = A x, the parts meet over distributed shared
+// memory, and each CTA adds its columns of B v.  Both products run on the tensor
+// cores with the weights as MMA rows and the tokens as columns, each weight word
+// loaded once, from memory into operand registers.  The adapter is read once, by
+// the cluster, and there is no second launch to wait for.  Bound by latency (two
+// chains of loads): 5.8 us for one token (rank 16, 4096 -> 4096), 23 us for 64 tokens
+// over 32 adapters of rank up to 64, 4096 -> 12288 (42 MB).
 //
-// More tokens: the tokens are sorted by adapter and cut into tiles of 64, and two
-// tensor-core kernels (mma.sync) follow.  Shrink: a tile is a cluster, its CTAs
-// and warps split the channels; the parts are summed over distributed shared
-// memory in a fixed order.  Expand: a warp holds 16 tokens' v as MMA operands
-// and streams over the columns.  Both are bound by memory (x once; base and y
-// once): the products have a few dozen terms per byte.
-// Precision: the tensor cores take 16-bit operands, so a binary32 value is cut
-// into three bfloat16 parts that sum to it exactly (8 significand bits each, by
-// truncation) and the products of parts are summed in binary32; of two cut
-// operands the products below 2^-24 are left out.  A binary16 weight is two
-// bfloat16 parts exactly.  In the expand kernel a binary16 weight is taken as it
+// More tokens: the tokens are sorted by adapter, and two tensor-core kernels
+// (mma.sync) follow.  Shrink: 16 tokens of one adapter per CTA (per cluster, where
+// that leaves SMs idle), its warps split rank and channels; the parts are summed in
+// a fixed order.  Expand: a tile of 64 tokens and a span of columns per CTA; a warp
+// holds 16 tokens' v as MMA operands and streams over the columns.  By their bytes
+// both are bound by memory (x once; base and y once: the products have a few
+// dozen terms per byte); measured, 2048 tokens, rank 64, 4096 -> 14336 in binary16
+// take 96 us (44 at a copy's rate): expand 60 us, 3.5 TB/s, held back by the
+// barriers of the shared weight ring, shrink 30 us, by the latency of its loads.
+// Precision: bfloat16 weights are taken as they are, and x, cut by truncation into
+// three bfloat16 parts that sum to it exactly (8 significand bits each).  binary16 and
+// binary32 operands of the shrink and decode kernels are cut into tf32 parts (11 bits
+// rounded, and the rest; a binary16 weight is one part); of two cut operands the
+// product of the two rests, below 2^-22, is left out.  The products of parts are summed in
+// binary32.  In the expand kernel a binary16 weight is taken as it
 // is, and v, scaled by a power of two per token into binary16's range, as two
 // binary16 parts (rounded: 2^-23 of v).
 #include <cooperative_groups.h>

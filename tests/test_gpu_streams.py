@@ -71,3 +71,17 @@ def test_scratch_is_not_handed_out_while_the_call_runs(name):
     torch.cuda.synchronize()
     for y in ys:
         assert torch.equal(y, ref)
+
+
+def test_weights_that_are_not_on_the_current_device_are_refused():
+    experts = sq.alloc_experts(2, 32, 128)
+    experts.keep = (experts.keep[0].cpu(),)
+    q = sq.quantize_act(torch.randn(4, 128, device="cuda"), None)
+    off = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
+    with pytest.raises(sq.SQError, match="experts are not on the current device"):
+        sq.grouped_linear(experts, *q, None, off)
+    bank = sq.LoraBank(torch.zeros(1, 8, 128, device="cuda"), torch.zeros(1, 16, 8, device="cuda"),
+                       torch.ones(1, device="cuda"))
+    bank.A = bank.A.cpu()
+    with pytest.raises(sq.SQError, match="adapters are not on the current device"):
+        sq.lora_add(bank, torch.zeros(4, 128, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda"))
