@@ -549,8 +549,11 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) 
 #pragma unroll
           for (int j = 0; j < NT; ++j) issue_w(j, k);
         }
+        const bool inside = 32 * s + 32 <= p.K;  // (the whole warp's)
+        if (!inside) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) finish_masked<VEC>(xr8[h], k, p.K, true);
+          for (int h = 0; h < 2; ++h) finish_masked<VEC>(xr8[h], k, p.K, true);
+        }
         if constexpr (Parts<W>::n == 1) {
           uint32_t xa[2][3][4];
 #pragma unroll
@@ -559,7 +562,7 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) 
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             if (r0 + 8 * j >= rank) break;
-            finish_masked<VEC>(wr8[j], k, p.K, r0 + 8 * j + gid < rank);
+            if (!inside || r0 + 8 * j + 8 > rank) finish_masked<VEC>(wr8[j], k, p.K, r0 + 8 * j + gid < rank);
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -580,7 +583,7 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) 
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             if (r0 + 8 * j >= rank) break;
-            finish_masked<VEC>(wr8[j], k, p.K, r0 + 8 * j + gid < rank);
+            if (!inside || r0 + 8 * j + 8 > rank) finish_masked<VEC>(wr8[j], k, p.K, r0 + 8 * j + gid < rank);
             float wv[8];
             wr8[j].floats(wv);
             if constexpr (AHEAD) issue_w(j, next);
