@@ -76,6 +76,7 @@ struct Params {
   int32_t* status;
   int cluster;  // CTAs per cluster
   int span;   // expand: columns per CTA
+  int self_sort;  // the shrink kernel sorts the ids
   int tiles;  // expand: CTAs along the tiles (the rest copy rows without adapter)
 };
 
@@ -488,10 +489,97 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) k_lora_decode(const Params 
 constexpr int kShrinkThreads = 512, kShrinkWarps = kShrinkThreads / 32;
 constexpr int kGroupTokens = 16;
 
+// Without a sort from the caller, up to this many tokens: every CTA of the shrink kernel
+// finds its group in the ids by itself (a count per adapter, one scan, one pass for
+// the members), and the groups together write the sort that the expand kernel reads.
+// 333 tokens over 5 adapters take 28.4 us so, 30.1 with a sorting launch before them; 512 over
+// 100 32.6 and 34.3, 512 over 8 34.8 and 35.4; 1000 over 300 36.6 and 35.4.
+constexpr int kSelfSortTokens = 512;
+
+struct Group {
+  int a, p0, cnt;  // adapter (-1: none), first place, tokens
+};
+// Group u of the ids; its tokens in members[].  counts: [S] ints, part: one per warp.
+// All threads of the CTA call it; the first CTA writes the offsets.
+__device__ Group find_group(const Params& p, int u, bool writes_order, int* counts, int* part, int* members) {
+  __shared__ Group found;
+  static_assert(2 * kShrinkThreads >= kMaxSegments && kSelfSortTokens <= 32767, "two adapters a thread, packed sums");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int s = threadIdx.x; s < p.S; s += kShrinkThreads) counts[s] = 0;
+  if (threadIdx.x == 0) found.a = -1;
+  __syncthreads();
+  const int span = (p.M + kShrinkThreads - 1) / kShrinkThreads * 32;  // tokens per warp
+  const int lo = min(p.M, warp * span), hi = min(p.M, lo + span);
+  auto id_of = [&](int i) {
+    const int id = i < hi ? __ldg(p.ids + i) : -1;
+    return id >= 0 && id < p.S ? id : id == -1 ? -1 : -2;
+  };
+  bool bad = false;
+  for (int i0 = lo; i0 < hi; i0 += 32) {
+    const int id = id_of(i0 + lane);
+    bad |= id == -2;
+    const uint32_t same = __match_any_sync(0xffffffffu, id);
+    if (id >= 0 && __ffs(same) - 1 == lane) atomicAdd(&counts[id], __popc(same));  // (a count: the order does not matter)
+  }
+  if (bad && blockIdx.x == 0) set_status(p.status, SQ_ERR_INVALID_ARG);
+  __syncthreads();
+  // exclusive sums of (groups << 16 | tokens) over the adapters, two a thread
+  int n[2], v[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int s = 2 * threadIdx.x + h;
+    n[h] = s < p.S ? counts[s] : 0;
+    v[h] = ((n[h] + kGroupTokens - 1) / kGroupTokens) << 16 | n[h];
+  }
+  int incl = v[0] + v[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  int excl = incl - v[0] - v[1];
+  for (int w = 0; w < warp; ++w) excl += part[w];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int s = 2 * threadIdx.x + h, g = u - (excl >> 16);
+    if (blockIdx.x == 0 && s <= p.S) const_cast<int32_t*>(p.offsets)[s] = excl & 0xffff;
+    if (n[h] > 0 && g >= 0 && g * kGroupTokens < n[h])
+      found = Group{s, (excl & 0xffff) + g * kGroupTokens, min(kGroupTokens, n[h] - g * kGroupTokens)};
+    if (n[h] > 0 && g >= 0 && g * kGroupTokens < n[h]) members[kGroupTokens] = g * kGroupTokens;  // rank of its first
+    excl += v[h];
+  }
+  if (blockIdx.x == 0 && threadIdx.x == kShrinkThreads - 1 && p.S >= 2 * kShrinkThreads)
+    const_cast<int32_t*>(p.offsets)[p.S] = excl & 0xffff;
+  __syncthreads();
+  const Group f = found;
+  if (f.a < 0) return f;
+  const int first = members[kGroupTokens];
+  int mine = 0;
+  for (int i0 = lo; i0 < hi; i0 += 32) mine += __popc(__ballot_sync(0xffffffffu, id_of(i0 + lane) == f.a));
+  if (lane == 0) part[warp] = mine;
+  __syncthreads();
+  int at = -first;
+  for (int w = 0; w < warp; ++w) at += part[w];
+  for (int i0 = lo; i0 < hi && at < kGroupTokens; i0 += 32) {
+    const bool is = id_of(i0 + lane) == f.a;
+    const uint32_t all = __ballot_sync(0xffffffffu, is);
+    const int r = at + __popc(all & ((1u << lane) - 1u));
+    if (is && r >= 0 && r < kGroupTokens) {
+      members[r] = i0 + lane;
+      if (writes_order) const_cast<int32_t*>(p.order)[f.p0 + r] = i0 + lane;
+    }
+    at += __popc(all);
+  }
+  __syncthreads();
+  return f;
+}
+
 template <class W, bool VEC>
 __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) {
   extern __shared__ __align__(16) float sm[];  // [slices][16][Rp], then the tile sums [S + 1]
-  __shared__ int part_i[kShrinkThreads / 32];
+  __shared__ int part_i[kShrinkThreads / 32], members[kGroupTokens + 1];
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = p.cluster, c = (int)cluster.block_rank(), u = (int)blockIdx.x / nc;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tid4 = lane & 3;
@@ -500,11 +588,19 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) 
   int* pre = reinterpret_cast<int*>(sm + warps * kGroupTokens * p.Rp);
   pdl_wait();
   pdl_launch_dependents();
-  const int units = segment_units(p.offsets, p.S, p.M, p.status, kGroupTokens, pre, part_i);
-  if (u >= units) return;  // (the whole cluster)
-  const int a = unit_expert(pre, p.S, u);
-  const int2 seg = segment_bounds(p.offsets, p.M, a, p.status);
-  const int p0 = seg.x + (u - pre[a]) * kGroupTokens, cnt = min(kGroupTokens, seg.y - p0);
+  Group group;
+  if (p.self_sort) {
+    group = find_group(p, u, c == 0, pre, part_i, members);
+    if (group.a < 0) return;  // (the whole cluster)
+  } else {
+    const int units = segment_units(p.offsets, p.S, p.M, p.status, kGroupTokens, pre, part_i);
+    if (u >= units) return;
+    group.a = unit_expert(pre, p.S, u);
+    const int2 seg = segment_bounds(p.offsets, p.M, group.a, p.status);
+    group.p0 = seg.x + (u - pre[group.a]) * kGroupTokens;
+    group.cnt = min(kGroupTokens, seg.y - group.p0);
+  }
+  const int a = group.a, p0 = group.p0, cnt = group.cnt;
   const int rank = adapter_rank(p, a);
   const int steps = (p.K + 31) / 32, slice = c * warps + part, slices = nc * warps;
   const int s0 = (int)((int64_t)steps * slice / slices), s1 = (int)((int64_t)steps * (slice + 1) / slices);
@@ -513,7 +609,8 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) 
     const float* xr[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      int t = __ldg(p.order + p0 + min(gid + 8 * h, cnt - 1));
+      const int at = min(gid + 8 * h, cnt - 1);
+      int t = p.self_sort ? members[at] : __ldg(p.order + p0 + at);
       if (t < 0 || t >= p.M) {
         set_status(p.status, SQ_ERR_INVALID_ARG);
         t = 0;
@@ -969,8 +1066,11 @@ cudaError_t launch_type(Params p, void* sort_ws, int32_t* sort_arrays, int sm_co
     int32_t* offsets = sort_arrays;
     int32_t* order = offsets + round_up(p.S + 1, 4);
     int32_t* place = order + round_up(p.M, 4);
-    const cudaError_t e = launch_segment(p.ids, p.M, p.S, offsets, order, place, sort_ws, p.status, stream);
-    if (e != cudaSuccess) return e;
+    p.self_sort = p.M <= kSelfSortTokens ? 1 : 0;
+    if (!p.self_sort) {
+      const cudaError_t e = launch_segment(p.ids, p.M, p.S, offsets, order, place, sort_ws, p.status, stream);
+      if (e != cudaSuccess) return e;
+    }
     p.offsets = offsets;
     p.order = order;
   }

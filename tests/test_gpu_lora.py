@@ -253,3 +253,20 @@ def test_the_most_tokens(M):
     v = (bank.A[at] * x[:, None, :]).sum(2) * bank.scale[at][:, None]
     want = base + torch.where(ids[:, None] >= 0, (bank.B[at] * v[:, None, :]).sum(2), 0.0)
     assert st.item() == 0 and torch.equal(y, want)
+
+
+@pytest.mark.parametrize("M,S", [(65, 1), (65, 1024), (300, 1023), (511, 40), (512, 1), (512, 1024), (513, 1024)])
+def test_a_sort_of_ones_own_gives_the_same_bits(M, S):
+    """The call's own sort (by launch or within the kernels) against segments()."""
+    c = Case(M, S, 16, 264, 72, "bf16")
+    y = c.run()
+    c.check(y)
+    z = c.run(segments=sq.segment(c.idsd, S))
+    assert torch.equal(y, z) and c.status.item() == 0
+
+
+@pytest.mark.parametrize("M", [100, 512, 600])
+def test_no_token_has_an_adapter(M):
+    c = Case(M, 3, 16, 264, 72, "f16")
+    c.idsd.fill_(-1)
+    assert torch.equal(c.run(), c.based) and c.status.item() == 0
