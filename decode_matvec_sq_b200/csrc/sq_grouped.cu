@@ -178,7 +178,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
   const int64_t V = (int64_t)groups * a.rbe;
   const int64_t share = fast_div(V + gridDim.x - 1, (int)gridDim.x), v0 = blockIdx.x * share;
   if (v0 >= V) return;
-  const int len = (int)min(share, V - v0) * a.tpr;  // tiles (the host keeps it in 32 bits)
+  // tiles: in 32 bits by the host's check of n, unless bad offsets (reported) let
+  // segments overlap; the rest of such a share is left out
+  const int len = (int)min(min(share, V - v0) * a.tpr, (int64_t)0x7fffffff);
   const int t0 = (int)(((int64_t)warp * len) >> 4), t1 = (int)(((int64_t)(warp + 1) * len) >> 4);
   static_assert(kWarps == 16, "the split over the warps");
   // this warp's first tile: row block rb of the expert of group u, channel group cg
