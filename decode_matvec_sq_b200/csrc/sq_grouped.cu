@@ -16,10 +16,10 @@
 // What bounds it: the weight stream.  Each warp keeps 2 D tiles (2.3 KB each) in
 // flight by bulk copies into its shared-memory ring, two tiles to a slot, one
 // mbarrier per slot.
-// Measured: one token through 2 of 8 experts, 4096 -> 14336, 26.3 us, 5.2 TB/s of the
-// packed weights, 0.79 of a copy's rate (what is missing: the launch, the walk over
-// the offsets and the drain, 5 us of the 26); 16 tokens, 2 of 8 each, 14336 -> 4096,
-// 72 outlier channels, 108 us, 5.0 TB/s.
+// Measured: one token through 2 of 8 experts, 4096 -> 14336, 26 to 28 us, 4.8 to 5.2 TB/s
+// of the packed weights, 0.74 to 0.79 of a copy's rate (what is missing: the launch, the
+// walk over the offsets and the drain, 5 us); 16 tokens, 2 of 8 each, 14336 -> 4096,
+// 72 outlier channels, 101 to 108 us, 5.0 to 5.3 TB/s.
 // The trunk operand is +-1 (0 outside the mask) bytes made from the bits by one
 // shift, one sign-replicating byte permute and one three-input logic operation
 // per four channels, so T needs one MMA where bits as 0/-1 need two.

@@ -23,8 +23,8 @@
 // holds 16 tokens' v as MMA operands and streams over the columns.  By their bytes
 // both are bound by memory (x once; base and y once: the products have a few
 // dozen terms per byte); measured, 2048 tokens, rank 64, 4096 -> 14336 in binary16
-// take 96 us (44 at a copy's rate): expand 60 us, 3.5 TB/s, held back by the
-// barriers of the shared weight ring, shrink 30 us, by the latency of its loads.
+// take 92 us (44 at a copy's rate): sort and shrink 35 to 40 us, chains of loads, the
+// expand kernel the rest, of which 48 us go to copying base and y alone.
 // Precision: bfloat16 weights are taken as they are, and x, cut by truncation into
 // three bfloat16 parts that sum to it exactly (8 significand bits each).  binary16 and
 // binary32 operands of the shrink and decode kernels are cut into tf32 parts (11 bits
