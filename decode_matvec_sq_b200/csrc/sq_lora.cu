@@ -29,8 +29,9 @@
 // three bfloat16 parts that sum to it exactly (8 significand bits each).  binary16 and
 // binary32 operands of the shrink and decode kernels are cut into tf32 parts (11 bits
 // rounded, and the rest; a binary16 weight is one part); of two cut operands the
-// product of the two rests, below 2^-22, is left out.  The products of parts are summed in
-// binary32.  In the expand kernel a binary16 weight is taken as it
+// product of the two rests, below 2^-22, is left out.  The products of parts are summed by
+// the tensor cores over at most 32 channels (or of the rank), those sums in binary32 with
+// rounding (add_step).  In the expand kernel a binary16 weight is taken as it
 // is, and v, scaled by a power of two per token into binary16's range, as two
 // binary16 parts (rounded: 2^-23 of v).
 #include <cooperative_groups.h>
@@ -95,6 +96,20 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A step's sums into the running ones.  The tensor cores add with truncation, always
+// towards zero, so an accumulator that stays there drifts with the number of steps
+// (rank 128: 1.3e-5 of the result at K = 14336, rank 256: 1.2e-4 at 65536); sums of one
+// step, added here with rounding, do not (the rms of the error is that of a binary32 sum).
+__device__ __forceinline__ void add_step(float (&acc)[4], const float (&t)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] += t[i];
+}
+// low: the products of the operands' lesser parts, kept from the larger sum.
+__device__ __forceinline__ void add_step(float (&acc)[4], const float (&t)[4], const float (&low)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] += t[i] + low[i];
 }
 
 // One k8 step on tf32 operands (the tensor cores read the upper 19 bits of each).
@@ -232,7 +247,7 @@ __device__ __forceinline__ void load_masked(Raw8<T>& r, const T* row, int i0, in
 // tokens its eight columns.  A lane holds the activations (then v) of token gid.
 // Each weight word is loaded once, from memory straight into operand registers.
 
-// acc (+ low) += A x over one 32-channel step: rows w0 (gid) and w1 (gid + 8), columns'
+// acc += A x over one 32-channel step: rows w0 (gid) and w1 (gid + 8), columns'
 // operand parts x.
 template <class W>
 struct Columns;
@@ -240,14 +255,17 @@ template <>
 struct Columns<__nv_bfloat16> {
   uint32_t p[3][4];
   __device__ __forceinline__ void set(float (&v)[8]) { cut8<3>(v, p); }
-  __device__ __forceinline__ void mma(float (&acc)[4], float (&)[4], const Raw8<__nv_bfloat16>& w0,
+  __device__ __forceinline__ void mma(float (&acc)[4], const Raw8<__nv_bfloat16>& w0,
                                       const Raw8<__nv_bfloat16>& w1) const {
+    float t[4] = {}, low[4] = {};
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const uint32_t a[4] = {w0.w[2 * q], w1.w[2 * q], w0.w[2 * q + 1], w1.w[2 * q + 1]};
-#pragma unroll
-      for (int i = 2; i >= 0; --i) mma_bf16(acc, a, p[i][2 * q], p[i][2 * q + 1]);
+      mma_bf16(low, a, p[2][2 * q], p[2][2 * q + 1]);
+      mma_bf16(low, a, p[1][2 * q], p[1][2 * q + 1]);
+      mma_bf16(t, a, p[0][2 * q], p[0][2 * q + 1]);
     }
+    add_step(acc, t, low);
   }
 };
 template <class W>
@@ -257,7 +275,8 @@ struct Columns32 {  // tf32 parts
 #pragma unroll
     for (int i = 0; i < 8; ++i) cut_tf32(v[i], h[i], l[i]);
   }
-  __device__ __forceinline__ void mma(float (&acc)[4], float (&low)[4], const Raw8<W>& w0, const Raw8<W>& w1) const {
+  __device__ __forceinline__ void mma(float (&acc)[4], const Raw8<W>& w0, const Raw8<W>& w1) const {
+    float t[4] = {}, low[4] = {};
     float f0[8], f1[8];
     w0.floats(f0);
     w1.floats(f1);
@@ -274,8 +293,9 @@ struct Columns32 {  // tf32 parts
         mma_tf32(low, b[0], b[1], b[2], b[3], h[2 * q], h[2 * q + 1]);
       }
       mma_tf32(low, a[0], a[1], a[2], a[3], l[2 * q], l[2 * q + 1]);
-      mma_tf32(acc, a[0], a[1], a[2], a[3], h[2 * q], h[2 * q + 1]);
+      mma_tf32(t, a[0], a[1], a[2], a[3], h[2 * q], h[2 * q + 1]);
     }
+    add_step(acc, t, low);
   }
 };
 template <>
@@ -368,7 +388,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) k_lora_decode(const Params 
     const int steps = (p.K + 31) / 32, slice = c * kWarps + warp, slices = nc * kWarps;
     const int s0 = (int)((int64_t)steps * slice / slices), s1 = (int)((int64_t)steps * (slice + 1) / slices);
     for (int r0 = 0; r0 < rank; r0 += 64) {
-      float acc[4][4] = {}, low[4][4] = {};
+      float acc[4][4] = {};
       for (int s = s0; s < s1; ++s) {
         const int k = 32 * s + 8 * tid4;
         Raw8<float> xr;
@@ -387,14 +407,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) k_lora_decode(const Params 
         x.set(xf);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (r0 + 16 * j < rank) x.mma(acc[j], low[j], w[j][0], w[j][1]);
+          if (r0 + 16 * j < rank) x.mma(acc[j], w[j][0], w[j][1]);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (r0 + 16 * j < rank) {
           float* o = part + (warp * R16 + r0 + 16 * j + gid) * 8 + 2 * tid4;
-          *reinterpret_cast<float2*>(o) = make_float2(acc[j][0] + low[j][0], acc[j][1] + low[j][1]);
-          *reinterpret_cast<float2*>(o + 64) = make_float2(acc[j][2] + low[j][2], acc[j][3] + low[j][3]);
+          *reinterpret_cast<float2*>(o) = make_float2(acc[j][0], acc[j][1]);
+          *reinterpret_cast<float2*>(o + 64) = make_float2(acc[j][2], acc[j][3]);
         }
     }
   }
@@ -435,7 +455,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) k_lora_decode(const Params 
   }
   constexpr int kAhead = 2;
   for (int b0 = n0 + 16 * kAhead * warp; b0 < n1; b0 += 16 * kAhead * kWarps) {
-    float b[kAhead][4], acc[kAhead][4] = {}, low[kAhead][4] = {};
+    float b[kAhead][4], acc[kAhead][4] = {};
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
 #pragma unroll
@@ -463,7 +483,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) k_lora_decode(const Params 
         Columns<W> v;
         v.set(vf);
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) v.mma(acc[u], low[u], w[e][u][0], w[e][u][1]);
+        for (int u = 0; u < kAhead; ++u) v.mma(acc[u], w[e][u][0], w[e][u][1]);
       }
     }
 #pragma unroll
@@ -471,7 +491,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) k_lora_decode(const Params 
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int n = b0 + 16 * u + gid + 8 * (i >> 1);
-        if (n < n1 && 2 * tid4 + (i & 1) < nm) yy[i & 1][n] = b[u][i] + (acc[u][i] + low[u][i]);
+        if (n < n1 && 2 * tid4 + (i & 1) < nm) yy[i & 1][n] = b[u][i] + acc[u][i];
       }
   }
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
@@ -618,11 +638,8 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) 
       xr[h] = p.x + (int64_t)t * p.K;
     }
     const W* Aa = static_cast<const W*>(p.A) + (int64_t)a * p.R * p.K;
-    // the products of leading parts, and the rest: an addition of the tensor cores
-    // may truncate, so the many small ones are kept from the large sum
-    constexpr bool SPLIT = Parts<W>::n > 1;
     constexpr int NT = 4;
-    float acc[NT][4] = {}, low[SPLIT ? NT : 1][4] = {};
+    float acc[NT][4] = {};
     if (r0 < rank && s0 < s1) {
       Raw8<float> xr8[2];
       Raw8<W> wr8[NT];
@@ -660,13 +677,15 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) 
           for (int j = 0; j < NT; ++j) {
             if (r0 + 8 * j >= rank) break;
             if (!inside || r0 + 8 * j + 8 > rank) finish_masked<VEC>(wr8[j], k, p.K, r0 + 8 * j + gid < rank);
+            float t[4] = {};
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int i = 2; i >= 0; --i)  // small products first
 #pragma unroll
-              for (int i = 2; i >= 0; --i) {  // small products first
+              for (int q = 0; q < 2; ++q) {
                 const uint32_t av[4] = {xa[0][i][2 * q], xa[1][i][2 * q], xa[0][i][2 * q + 1], xa[1][i][2 * q + 1]};
-                mma_bf16(acc[j], av, wr8[j].w[2 * q], wr8[j].w[2 * q + 1]);
+                mma_bf16(t, av, wr8[j].w[2 * q], wr8[j].w[2 * q + 1]);
               }
+            add_step(acc[j], t);
             issue_w(j, next);
           }
         } else {
@@ -684,6 +703,7 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) 
             float wv[8];
             wr8[j].floats(wv);
             if constexpr (AHEAD) issue_w(j, next);
+            float t[4] = {}, low[4] = {};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint32_t h0 = __float_as_uint(wv[2 * q]), h1 = __float_as_uint(wv[2 * q + 1]);
@@ -691,20 +711,15 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) 
                 uint32_t l0, l1;
                 cut_tf32(wv[2 * q], h0, l0);
                 cut_tf32(wv[2 * q + 1], h1, l1);
-                mma_tf32(low[SPLIT ? j : 0], xh[0][2 * q], xh[1][2 * q], xh[0][2 * q + 1], xh[1][2 * q + 1], l0, l1);
+                mma_tf32(low, xh[0][2 * q], xh[1][2 * q], xh[0][2 * q + 1], xh[1][2 * q + 1], l0, l1);
               }
-              mma_tf32(low[SPLIT ? j : 0], xl[0][2 * q], xl[1][2 * q], xl[0][2 * q + 1], xl[1][2 * q + 1], h0, h1);
-              mma_tf32(acc[j], xh[0][2 * q], xh[1][2 * q], xh[0][2 * q + 1], xh[1][2 * q + 1], h0, h1);
+              mma_tf32(low, xl[0][2 * q], xl[1][2 * q], xl[0][2 * q + 1], xl[1][2 * q + 1], h0, h1);
+              mma_tf32(t, xh[0][2 * q], xh[1][2 * q], xh[0][2 * q + 1], xh[1][2 * q + 1], h0, h1);
             }
+            add_step(acc[j], t, low);
           }
         }
       }
-    }
-    if constexpr (SPLIT) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] += low[j][i];
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -940,17 +955,25 @@ __global__ void __launch_bounds__(kExpandThreads, 4) k_lora_expand(const Params 
 #pragma unroll
       for (int i = 0; i < NV; ++i) va[i] = vw[(s * NV + i) * 32 + lane];
       if constexpr (BF || HALF) {
+        // (four columns' sums side by side: one after another, their chains of MMAs cost 5 us more)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j0 = 0; j0 < 8; j0 += 4) {
+          float t[4][4] = {};
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+          for (int i = NV / 2 - 1; i >= 0; --i)  // small products first
 #pragma unroll
-            for (int i = NV / 2 - 1; i >= 0; --i) {  // small products first
+            for (int q = 0; q < 2; ++q) {
               const uint4 f = va[i * 2 + q];
               const uint32_t av[4] = {f.x, f.y, f.z, f.w};
-              if constexpr (HALF) mma_f16(acc[j], av, wr8[j].w[2 * q], wr8[j].w[2 * q + 1]);
-              else mma_bf16(acc[j], av, wr8[j].w[2 * q], wr8[j].w[2 * q + 1]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if constexpr (HALF) mma_f16(t[j], av, wr8[j0 + j].w[2 * q], wr8[j0 + j].w[2 * q + 1]);
+                else mma_bf16(t[j], av, wr8[j0 + j].w[2 * q], wr8[j0 + j].w[2 * q + 1]);
+              }
             }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) add_step(acc[j0 + j], t[j]);
+        }
       } else {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -964,9 +987,11 @@ __global__ void __launch_bounds__(kExpandThreads, 4) k_lora_expand(const Params 
             uint32_t h0, h1, l0, l1;
             cut_tf32(__uint_as_float(wr8[j].w[2 * q]), h0, l0);
             cut_tf32(__uint_as_float(wr8[j].w[2 * q + 1]), h1, l1);
-            mma_tf32(acc[j], vh[0], vh[1], vh[2], vh[3], l0, l1);
-            mma_tf32(acc[j], vl[0], vl[1], vl[2], vl[3], h0, h1);
-            mma_tf32(acc[j], vh[0], vh[1], vh[2], vh[3], h0, h1);
+            float t[4] = {};
+            mma_tf32(t, vh[0], vh[1], vh[2], vh[3], l0, l1);
+            mma_tf32(t, vl[0], vl[1], vl[2], vl[3], h0, h1);
+            mma_tf32(t, vh[0], vh[1], vh[2], vh[3], h0, h1);
+            add_step(acc[j], t);
           }
         }
       }
