@@ -93,4 +93,18 @@ __device__ __forceinline__ int expand_nibble(uint32_t bits) {
   return (int)(((bits & 0xFu) * 0x00204081u) & 0x01010101u);
 }
 
+// v = hi + lo for tf32 products: hi rounded to tf32's 11 bits (a value that would round
+// to infinity, from 2^128 - 2^116 on, to the largest finite one), lo the exact rest, of
+// which the tensor cores read 11 bits.
+__device__ __forceinline__ void cut_tf32(float v, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rna.satfinite.tf32.f32 %0, %1;" : "=r"(hi) : "f"(v));
+  lo = __float_as_uint(v - __uint_as_float(hi));
+}
+__device__ __forceinline__ void cut_tf32(float v, float& hi, float& lo) {
+  uint32_t h, l;
+  cut_tf32(v, h, l);
+  hi = __uint_as_float(h);
+  lo = __uint_as_float(l);
+}
+
 }  // namespace sq

@@ -132,14 +132,6 @@ __device__ __forceinline__ void mma_tf32(uint32_t d, uint64_t a, uint64_t b, uin
       "tcgen05.mma.cta_group::1.kind::tf32 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0));
 }
-// v = hi + lo: hi rounded to tf32's 11 bits, lo the exact rest (of which the tensor
-// cores read 11 bits).
-__device__ __forceinline__ void cut_tf32(float v, float& hi, float& lo) {
-  uint32_t h;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(h) : "f"(v));
-  hi = __uint_as_float(h);
-  lo = v - hi;
-}
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Aux* aux, const Params& p) {
   // (the clock is read once in 32 tries: reading it at every one slows the SM)

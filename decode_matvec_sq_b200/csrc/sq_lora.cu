@@ -120,11 +120,6 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// v = hi + lo: hi rounded to tf32's 11 bits, lo the exact rest.
-__device__ __forceinline__ void cut_tf32(float v, uint32_t& hi, uint32_t& lo) {
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(v));
-  lo = __float_as_uint(v - __uint_as_float(hi));
-}
 
 // Upper halves of two binary32 values as a pair of bfloat16 (first in the low half).
 __device__ __forceinline__ uint32_t upper_pair(float a, float b) {
