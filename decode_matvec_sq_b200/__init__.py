@@ -23,6 +23,7 @@ HEADER = os.path.join(os.path.dirname(PKG_DIR), "include", "sq.h")
 
 SQ_LAUNCH_PDL = 1
 SQ_TRUNK_ONLY = 2
+SQ_ZERO_REST = 4
 SQ_LAYOUT_ROWS = 0
 SQ_LAYOUT_TILES = 1
 SQ_LAYOUT_TILES_SPARSE = 2
@@ -781,7 +782,8 @@ def grouped_linear(experts: PackedExperts, xq, sx, x_out, idx, offsets, order=No
                    workspace=None, status=None, pdl: bool = False, stream=None):
     """y [n][N] float32: place p of segment e is expert e's weight times the
     activations (as from quantize_act) of row order[p] // div, or of row p
-    without an order.  Rows from offsets[E] on are not written."""
+    without an order.  The rows from offsets[E] on (of dropped entries) are 0 in a
+    result allocated here, and not written in a `y` given."""
     import torch
     if stream is not None:
         return _on(stream, grouped_linear, experts, xq, sx, x_out, idx, offsets, order, div, y, workspace, status, pdl)
@@ -802,14 +804,16 @@ def grouped_linear(experts: PackedExperts, xq, sx, x_out, idx, offsets, order=No
     n = rows if order is None else order.numel()
     dp = _opt(order, i32, (n,), cur, w, "order")
     fp = _arg(offsets, i32, (E + 1,), cur, w, "offsets")
+    flags = _flags(pdl)
     if y is None:
         y = torch.empty(n, N, dtype=f32, device=xq.device)
+        flags |= SQ_ZERO_REST  # (a quantize_act before the next layer reads every row)
     yp = _arg(y, f32, (n, N), cur, w, "y")
     L = lib()
     need = 0 if workspace is not None else grouped_workspace_bytes(experts, n)
     workspace, wp, wn = _workspace_arg(workspace, need, xq.device, cur, w)
     rc = L.sq_grouped_linear(ctypes.byref(experts.view), E, N, xp, sp, op, ip, nout, rows, dp, div, fp, n, yp, wp,
-                             wn, _status_arg(status, cur, w), _flags(pdl), _stream_arg(cur))
+                             wn, _status_arg(status, cur, w), flags, _stream_arg(cur))
     if rc:
         _ck(rc, w)
     return y

@@ -716,7 +716,7 @@ static sq_status grouped_linear(const sq_packed_weight* stack, int32_t E, int32_
   if ((int64_t)n * (tiles_rows(N) / kTileRows) >= (1ll << 40) / (tiles_cols(stack->K) / kTileK)) return SQ_ERR_SHAPE;
   if (n_out < 0 || n_out > kMaxOutliers || n_out > stack->K) return SQ_ERR_SHAPE;
   if (n_out > 0 && (!idx || !x_out)) return SQ_ERR_INVALID_ARG;
-  if (flags & ~SQ_LAUNCH_PDL) return SQ_ERR_INVALID_ARG;
+  if (flags & ~(SQ_LAUNCH_PDL | SQ_ZERO_REST)) return SQ_ERR_INVALID_ARG;
   if (!aligned16(xq) || !aligned16(sx) || !aligned16(offsets) || !aligned16(y) || (order && !aligned16(order)) ||
       (n_out > 0 && (!aligned16(idx) || !aligned16(x_out))) || (workspace && !aligned16(workspace)))
     return SQ_ERR_ALIGN;
@@ -750,6 +750,7 @@ static sq_status grouped_linear(const sq_packed_weight* stack, int32_t E, int32_
   a.y = y;
   a.status = dev_status;
   a.pdl = (flags & SQ_LAUNCH_PDL) ? 1 : 0;
+  a.zero_rest = (flags & SQ_ZERO_REST) ? 1 : 0;
   a.wait_ns = wait_ns;
   a.skip_group = skip_group;
   return from_cuda(launch_grouped(a, workspace, d.sm_count, static_cast<cudaStream_t>(stream)));

@@ -177,7 +177,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
   // gives for as many CTAs as it takes, so that no CTA finishes alone
   const int64_t V = (int64_t)groups * a.rbe;
   const int64_t share = fast_div(V + gridDim.x - 1, (int)gridDim.x), v0 = blockIdx.x * share;
-  if (v0 >= V) return;
+  if (v0 >= V) {
+    if (a.zero_rest) zero_rest(a);
+    return;
+  }
   // tiles: in 32 bits by the host's check of n, unless bad offsets (reported) let
   // segments overlap; the rest of such a share is left out
   const int len = (int)min(min(share, V - v0) * a.tpr, (int64_t)0x7fffffff);
@@ -237,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped(const Params p) {
     enter_rows();
   }
   for (int d = 0; d < D; ++d) copy(d);
+  if (a.zero_rest) zero_rest(a);
 
   // the outlier tables, while the first tiles are on their way
   bool bad = i0 < a.n_out && (jv < 0 || jv >= a.K || jp >= jv);

@@ -34,6 +34,7 @@ struct GroupedArgs {
   float* y;
   int32_t* status;
   int pdl;
+  int zero_rest;        // rows of y behind the last segment become 0
   // for the tests (include/sq_testing.h): the limit of the many-token kernel's waits,
   // and a channel group whose weights are never requested (-1: none)
   uint64_t wait_ns;
@@ -76,6 +77,14 @@ __device__ __forceinline__ int source_row(const GroupedArgs& p, int at) {
     r = 0;
   }
   return r;
+}
+
+// The rows of y behind the last segment set to 0, one CTA a row (all threads of every
+// CTA call it; rows of no segment, so nothing else writes them).
+__device__ __forceinline__ void zero_rest(const GroupedArgs& p) {
+  const int live = min(max(__ldg(p.offsets + p.E), 0), p.n);
+  for (int64_t r = (int64_t)live + blockIdx.x; r < p.n; r += gridDim.x)
+    for (int c = threadIdx.x; c < p.N; c += blockDim.x) p.y[r * p.N + c] = 0.0f;
 }
 
 // Exclusive sums over the experts of ceil(segment / unit), into pre[0 .. E]

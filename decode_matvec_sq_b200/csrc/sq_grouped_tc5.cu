@@ -719,6 +719,7 @@ __global__ void __launch_bounds__(256) k_grouped_rows(const GroupedArgs a, int8_
     }
     if (bad) set_status(a.status, SQ_ERR_INVALID_ARG);
   }
+  if (a.zero_rest) zero_rest(a);
   const int live = min(max(__ldg(a.offsets + a.E), 0), a.n);
   for (int p = blockIdx.x * 8 + (threadIdx.x >> 5); p < live; p += gridDim.x * 8) {
     const int r = source_row(a, p);

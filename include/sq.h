@@ -55,6 +55,7 @@ typedef enum {
 /* Launch flags (bit set). */
 #define SQ_LAUNCH_PDL 1u
 #define SQ_TRUNK_ONLY 2u
+#define SQ_ZERO_REST 4u
 /* SQ_TRUNK_ONLY (sq_linear, sq_quantize_linear, sq_linear_noalloc; weights in
  * SQ_LAYOUT_TILES or SQ_LAYOUT_TILES_SPARSE only, else SQ_ERR_INVALID_ARG):
  * the residual path is
@@ -547,7 +548,10 @@ sq_status sq_expert_view(const sq_packed_weight *stack, int32_t E, int32_t N, in
  *   offsets     [E+1] i32, device, ascending from 0; the segments may be empty
  *   n           places: offsets[E] <= n, order has n entries, 1 <= n <= 2^24 and
  *               n * roundup(N,16) * roundup(K,128) < 2^51
- *   y           [n][N] f32 out; the rows from offsets[E] on are left as they were
+ *   y           [n][N] f32 out; the rows from offsets[E] on are left as they were, or
+ *               set to 0 with SQ_ZERO_REST: for a call that reads all rows next, as
+ *               sq_quantize_act does between two layers (what old memory holds there
+ *               could be reported as SQ_ERR_NONFINITE)
  *   workspace   sq_grouped_linear_workspace_bytes bytes (may be 0), 16-byte
  *               aligned; scratch, it needs no zeroing.  Calls that may overlap
  *               in time (other streams, other captured graphs) need their own.
@@ -558,7 +562,7 @@ sq_status sq_expert_view(const sq_packed_weight *stack, int32_t E, int32_t N, in
  * Device-side findings: offsets that do not ascend in [0, n], an order entry
  * outside the activation rows and an index list that is not strictly ascending in
  * [0, K) set SQ_ERR_INVALID_ARG; nothing outside the arrays is touched.
- * flags: SQ_LAUNCH_PDL.
+ * flags: SQ_LAUNCH_PDL and/or SQ_ZERO_REST.
  */
 size_t sq_grouped_linear_workspace_bytes(const sq_packed_weight *stack, int32_t E, int32_t N, int32_t n);
 sq_status sq_grouped_linear(const sq_packed_weight *stack, int32_t E, int32_t N, const int8_t *xq,

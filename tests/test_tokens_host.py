@@ -143,3 +143,15 @@ def test_lora_refusals(L):
 
 def test_combine_refuses_more_columns_than_a_grid_holds(L):
     assert L.sq_combine(P, 8, P, P, 4, 2, 65535 * 256 + 1, None, P, None, 0, None) == 2
+
+
+def test_grouped_linear_flags(L):
+    """SQ_ZERO_REST passes the check of flags (the next one, of alignment, refuses the
+    call); bits without a meaning do not."""
+    v = _stack(L)
+
+    def call(flags):
+        return L.sq_grouped_linear(ctypes.byref(v), 4, 30, P, P, P, P, 2, 8, P, 2, P, 16, P, BAD, 0, None, flags, None)
+    assert call(sq.SQ_ZERO_REST) == 3 and call(sq.SQ_ZERO_REST | sq.SQ_LAUNCH_PDL) == 3
+    for flags in (sq.SQ_TRUNK_ONLY, 8, 1 << 31):
+        assert call(flags) == 1
