@@ -190,11 +190,14 @@ class PackedWeight:
     group_size: int
     with_mask: bool
     layout: int
-    buf: object                 # torch.uint8 device tensor
+    buf: object                 # torch.uint8 device tensor (of an expert: a tensor of its stack)
     view: SqPackedWeight
+    arrays: dict = None         # an expert of a stack: its rows of the stack's arrays (kept alive here)
 
     @property
     def nbytes(self) -> int:
+        if self.arrays is not None:
+            return sum(t.numel() * t.element_size() for t in self.arrays.values())
         return int(self.buf.numel())
 
     @property
@@ -208,6 +211,8 @@ class PackedWeight:
 
     def _arr(self, field: str, dtype, shape):
         import torch
+        if self.arrays is not None:
+            return self.arrays[field].view(*shape)
         base = self.buf.data_ptr()
         off = getattr(self.view, field) - base
         count = 1
@@ -710,7 +715,9 @@ def segment(ids, S: int, workspace=None, status=None, pdl: bool = False, stream=
 @dataclass
 class PackedExperts:
     """E experts of shape [N][K] in one packed weight (include/sq.h
-    sq_expert_view); ``keep`` holds the device tensors its view points into."""
+    sq_expert_view); ``keep`` holds the device tensors its view points into: one
+    allocation, or the arrays in the order of ARRAYS (None: absent)."""
+    ARRAYS = ("sign_bits", "alpha", "res_q", "res_scale", "mask_bits", "res_zero")
     E: int
     N: int
     K: int
@@ -719,12 +726,22 @@ class PackedExperts:
 
     def expert(self, e: int) -> PackedWeight:
         """Expert e as a packed weight of its own: decompose into it, or use it
-        with every call on one weight."""
+        with every call on one weight.  It keeps the stack's memory alive."""
         v = SqPackedWeight()
         _ck(lib().sq_expert_view(ctypes.byref(self.view), self.E, self.N, e, ctypes.byref(v)),
             "sq_expert_view")
-        buf = self.keep[0] if len(self.keep) == 1 else None
-        return PackedWeight(self.N, self.K, 128, bool(v.mask_bits), v.layout, buf, v)
+        rows = round_up(self.N, 16)
+        mine = {name: t[e * rows:(e + 1) * rows] for name, t in self._arrays().items()}
+        return PackedWeight(self.N, self.K, 128, bool(v.mask_bits), v.layout, self.keep[0], v, mine)
+
+    def _arrays(self) -> dict:
+        """The stack's arrays by name, a row of the stack in each row."""
+        if len(self.keep) > 1:
+            return {name: t for name, t in zip(self.ARRAYS, self.keep) if t is not None}
+        w = PackedWeight(self.view.N, self.K, 128, bool(self.view.mask_bits), self.view.layout, self.keep[0], self.view)
+        arrays = {"sign_bits": w.sign_bits(), "alpha": w.alpha(), "res_q": w.res_q(), "res_scale": w.res_scale(),
+                  "mask_bits": w.mask_bits(), "res_zero": w.res_zero()}
+        return {name: t for name, t in arrays.items() if t is not None}
 
 
 def alloc_experts(E: int, N: int, K: int, with_mask: bool = False, layout: int = SQ_LAYOUT_TILES,
@@ -764,7 +781,7 @@ def experts_from_arrays(E: int, N: int, K: int, sign_bits, alpha, res_q, res_sca
     v.res_zero = _opt(res_zero, torch.int32, (rows, cols // 128), cur, w, "res_zero")
     e0 = SqPackedWeight()
     _ck(lib().sq_expert_view(ctypes.byref(v), E, N, 0, ctypes.byref(e0)), w)  # the library's own checks
-    return PackedExperts(E, N, K, v, (sign_bits, alpha, res_q, res_scale, mask_bits, res_zero))
+    return PackedExperts(E, N, K, v, (sign_bits, alpha, res_q, res_scale, mask_bits, res_zero))  # (ARRAYS)
 
 
 def grouped_workspace_bytes(experts: PackedExperts, n: int) -> int:

@@ -155,3 +155,75 @@ def test_grouped_linear_flags(L):
     assert call(sq.SQ_ZERO_REST) == 3 and call(sq.SQ_ZERO_REST | sq.SQ_LAUNCH_PDL) == 3
     for flags in (sq.SQ_TRUNK_ONLY, 8, 1 << 31):
         assert call(flags) == 1
+
+
+def _stack_of_arrays(E, N, K, mask, asym):
+    """A stack over six host arrays with counting contents (addresses only: no device)."""
+    import torch
+    rows, cols = E * sq.round_up(N, 16), sq.round_up(K, 128)
+
+    def count(dtype, *shape):
+        n = 1
+        for s in shape:
+            n *= s
+        return (torch.arange(n) % 127).to(dtype).reshape(shape)
+    arrays = (count(torch.int32, rows, cols // 32), count(torch.float32, rows), count(torch.int8, rows, cols),
+              count(torch.float32, rows, cols // 128) + 1, count(torch.int32, rows, cols // 32) + 2 if mask else None,
+              count(torch.int32, rows, cols // 128) + 3 if asym else None)
+    v = sq.SqPackedWeight()
+    v.N, v.K, v.group_size = rows, K, 128
+    v.layout = sq.SQ_LAYOUT_TILES_ASYM if asym else sq.SQ_LAYOUT_TILES
+    v.sign_stride, v.res_stride, v.scale_stride = cols // 32, cols, cols // 128
+    v.sign_bits, v.alpha, v.res_q, v.res_scale, v.mask_bits, v.res_zero = (
+        None if t is None else t.data_ptr() for t in arrays)
+    return sq.PackedExperts(E, N, K, v, arrays)
+
+
+@pytest.mark.parametrize("mask,asym", [(0, 0), (1, 0), (0, 1), (1, 1)])
+def test_an_expert_of_given_arrays_keeps_them_alive(L, mask, asym):
+    """Every address in an expert's view lies in memory that the expert itself holds."""
+    import gc
+    stack = _stack_of_arrays(3, 30, 300, mask, asym)
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in stack.keep if t is not None]
+    pw = stack.expert(1)
+    del stack
+    gc.collect()
+    held = {pw.sign_bits().data_ptr(), pw.alpha().data_ptr(), pw.res_q().data_ptr(), pw.res_scale().data_ptr()}
+    held |= {t.data_ptr() for t in (pw.mask_bits(), pw.res_zero()) if t is not None}
+    view = {a for a in (pw.view.sign_bits, pw.view.alpha, pw.view.res_q, pw.view.res_scale, pw.view.mask_bits,
+                        pw.view.res_zero) if a}
+    assert view == held and len(view) == 4 + mask + asym
+    assert all(any(a <= p < b for a, b in spans) for p in view)
+
+
+@pytest.mark.parametrize("mask,asym", [(0, 0), (1, 1)])
+def test_the_arrays_of_an_expert(L, mask, asym):
+    """The accessors of an expert show its rows of the stack, and nbytes counts them."""
+    import torch
+    stack = _stack_of_arrays(3, 30, 300, mask, asym)
+    pw, at = stack.expert(2), slice(64, 96)
+    sign, alpha, res_q, res_scale, mask_bits, res_zero = stack.keep
+    assert torch.equal(pw.sign_bits(), sign[at]) and torch.equal(pw.alpha(), alpha[64:94])
+    assert torch.equal(pw.res_q(), res_q[at]) and torch.equal(pw.res_scale(), res_scale[at])
+    assert torch.equal(pw.mask_bits(), mask_bits[at]) if mask else pw.mask_bits() is None
+    assert torch.equal(pw.res_zero(), res_zero[at]) if asym else pw.res_zero() is None
+    assert pw.nbytes * 3 == sum(t.numel() * t.element_size() for t in stack.keep if t is not None)
+
+
+@pytest.mark.parametrize("layout,mask", [(sq.SQ_LAYOUT_TILES, False), (sq.SQ_LAYOUT_TILES_ASYM, True)])
+def test_the_arrays_of_an_expert_of_one_allocation(L, layout, mask):
+    import torch
+    n = sq.packed_bytes(96, 300, 128, mask, layout)
+    buf = torch.zeros(n + 256, dtype=torch.uint8)
+    buf = buf[-buf.data_ptr() % 256:][:n]
+    stack = sq.PackedExperts(3, 30, 300, sq.SqPackedWeight(), (buf,))
+    assert L.sq_packed_view(ctypes.c_void_p(buf.data_ptr()), 96, 300, 128, int(mask), layout, ctypes.byref(stack.view)) == 0
+    pw = stack.expert(1)
+    v = pw.view
+    for t, p, rows in ((pw.sign_bits(), v.sign_bits, 32), (pw.alpha(), v.alpha, 30), (pw.res_q(), v.res_q, 32),
+                       (pw.res_scale(), v.res_scale, 32), (pw.mask_bits(), v.mask_bits, 32), (pw.res_zero(), v.res_zero, 32)):
+        assert (t is None) == (not p)
+        if t is not None:
+            assert t.data_ptr() == p and t.shape[0] == rows
+    assert pw.buf is stack.keep[0]
+    assert pw.nbytes == 32 * (384 + 12 * 4 + 4 + 3 * 4 + (12 * 4 if mask else 0) + (12 if layout == sq.SQ_LAYOUT_TILES_ASYM else 0))
