@@ -452,18 +452,23 @@ cudaError_t with_lanes(int E, F f) {
   return f(std::integral_constant<int, 32>{});
 }
 
-// Entries per chunk of a two-launch sort: about 128 chunks (each of the second
-// launch's CTAs reads every chunk's counts), a multiple of `unit` entries.
+// Entries per chunk of a two-launch sort, a multiple of `unit`: at most kChunks chunks
+// (each of the second launch's CTAs reads every chunk's counts) up to kChunks full chunks;
+// more entries take more chunks, and the reads of counts grow with their square.
+constexpr int kChunks = 128;
+int longest_chunk(int unit) { return kMaxChunk / unit * unit; }  // (unit <= kMaxChoices)
 int chunk_entries(int64_t n, int unit) {
-  const int64_t want = std::min<int64_t>(kMaxChunk, std::max<int64_t>(256, ceil_div(n, 128)));
-  return (int)std::min<int64_t>(std::max<int64_t>(1, kMaxChunk / unit) * unit, round_up(want, unit));
+  const int64_t want = std::max<int64_t>(256, ceil_div(n, kChunks));
+  return (int)std::min<int64_t>(longest_chunk(unit), round_up(want, unit));
 }
 
 }  // namespace
 
 size_t segment_workspace_bytes(int64_t n, int S, int unit, bool route) {
   if (route ? n / unit <= kSmallTokens && n <= kMaxChunk : n <= kMaxChunk) return 0;
-  return (size_t)ceil_div(n, chunk_entries(n, unit)) * S * sizeof(int32_t);
+  // (the chunks themselves can be fewer for a longer sort, where rounding to `unit` makes
+  // them longer; a workspace for the longest batch serves every shorter one)
+  return (size_t)std::max<int64_t>(kChunks, ceil_div(n, longest_chunk(unit))) * S * sizeof(int32_t);
 }
 
 cudaError_t launch_route(const float* logits, int T, int E, int k, bool all, int32_t* ids, float* gates,

@@ -227,3 +227,29 @@ def test_the_arrays_of_an_expert_of_one_allocation(L, layout, mask):
             assert t.data_ptr() == p and t.shape[0] == rows
     assert pw.buf is stack.keep[0]
     assert pw.nbytes == 32 * (384 + 12 * 4 + 4 + 3 * 4 + (12 * 4 if mask else 0) + (12 if layout == sq.SQ_LAYOUT_TILES_ASYM else 0))
+
+
+def test_a_sort_workspace_serves_every_shorter_call(L):
+    """One allocation for the longest batch: the size does not fall as the batch grows."""
+    for k in (1, 2, 3, 5, 7, 8, 12, 31, 32):
+        for E in (32, 33, 128, 1024):
+            longest = 0
+            for T in sorted({*range(1, 700), *range(700, 9000, 7), *range(9000, (1 << 24) // k, 40009), (1 << 24) // k}):
+                need = L.sq_route_workspace_bytes(T, E, k)
+                assert need >= longest, (T, E, k)
+                longest = need
+    longest = 0
+    for n in sorted({*range(4000, 140000, 11), *range(140000, 1 << 24, 9973), 1 << 24}):
+        need = L.sq_segment_workspace_bytes(n, 77)
+        assert need >= longest, n
+        longest = need
+
+
+def test_an_adapter_workspace_serves_every_shorter_call(L):
+    for S, R in ((1, 8), (77, 33), (1024, 256)):
+        b = sq.SqLoraBank(S=S, R=R, K=256, N=512, type=sq.SQ_TYPE_BF16, A=1 << 41, B=1 << 41, scale=1 << 41, rank=None)
+        longest = 0
+        for M in (*range(1, 6000, 3), *range(6000, 1 << 20, 1013), 1 << 20):
+            need = L.sq_lora_workspace_bytes(ctypes.byref(b), M)
+            assert need >= longest, (S, R, M)
+            longest = need
