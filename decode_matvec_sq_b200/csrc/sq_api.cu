@@ -764,6 +764,22 @@ sq_status sq_grouped_linear(const sq_packed_weight* stack, int32_t E, int32_t N,
                         dev_status, flags, stream, kGroupedWaitNs, -1);
 }
 
+// Whether rows of na floats, lda apart from a on, share an element with rows of nb floats,
+// ldb apart from b on (M rows each; addresses of floats).
+static bool rows_overlap(const float* pa, int64_t lda, int64_t na, const float* pb, int64_t ldb, int64_t nb, int64_t M) {
+  const int64_t a = (int64_t)(reinterpret_cast<uintptr_t>(pa) / 4), b = (int64_t)(reinterpret_cast<uintptr_t>(pb) / 4);
+  if (a + (M - 1) * lda + na <= b || b + (M - 1) * ldb + nb <= a) return false;
+  // with equal strides only the distance of two rows counts: the first and the last row
+  // of a see every one
+  const int64_t step = lda == ldb ? std::max<int64_t>(1, M - 1) : 1;
+  for (int64_t i = 0; i < M; i += step) {
+    const int64_t row = a + i * lda, d = row - nb - b;  // the first row of b that ends behind `row`
+    const int64_t j = d < 0 ? 0 : d / ldb + 1;
+    if (j < M && b + j * ldb < row + na) return true;
+  }
+  return false;
+}
+
 sq_status sq_combine(const float* z, int32_t rows, const float* gates, const int32_t* place, int32_t T, int32_t k,
                      int32_t N, const float* base, float* out, int32_t* dev_status, uint32_t flags, void* stream) {
   if (!z || !gates || !place || !out) return SQ_ERR_INVALID_ARG;
@@ -773,6 +789,10 @@ sq_status sq_combine(const float* z, int32_t rows, const float* gates, const int
   if (flags & ~SQ_LAUNCH_PDL) return SQ_ERR_INVALID_ARG;
   if (!aligned16(z) || !aligned16(gates) || !aligned16(place) || !aligned16(out) || (base && !aligned16(base)))
     return SQ_ERR_ALIGN;
+  const int64_t words = (int64_t)T * N;
+  if (rows_overlap(out, words, words, z, (int64_t)rows * N, (int64_t)rows * N, 1) ||
+      (base && base != out && rows_overlap(out, words, words, base, words, words, 1)))
+    return SQ_ERR_INVALID_ARG;
   DeviceInfo d;
   sq_status st = check_device(&d);
   if (st != SQ_OK) return st;
@@ -813,6 +833,9 @@ sq_status sq_lora_add(const sq_lora_bank* bank, const float* x, int32_t M, const
     return SQ_ERR_ALIGN;
   const size_t need = lora_workspace_bytes(M, bank->S, bank->R);
   if (need && (!workspace || ws_bytes < need)) return SQ_ERR_WORKSPACE;
+  if ((base && base != y && rows_overlap(base, ld_base, bank->N, y, ld_y, bank->N, M)) ||
+      (!(x == y && (ld_y == bank->K || M == 1)) && rows_overlap(x, bank->K, bank->K, y, ld_y, bank->N, M)))
+    return SQ_ERR_INVALID_ARG;
   DeviceInfo d;
   if ((st = check_device(&d)) != SQ_OK) return st;
   return from_cuda(launch_lora(*bank, x, M, ids, offsets, order, base, ld_base, y, ld_y, workspace, dev_status, d.sm_count,

@@ -579,7 +579,8 @@ sq_status sq_grouped_linear(const sq_packed_weight *stack, int32_t E, int32_t N,
  *          is not used; a place outside [-1, rows) counts as -1 and sets
  *          SQ_ERR_INVALID_ARG)
  *   base   [T][N] f32, or NULL (then 0); may be out itself
- *   out    [T][N] f32; may not overlap z
+ *   out    [T][N] f32; may overlap neither z nor, unless it is base, base
+ *          (SQ_ERR_INVALID_ARG)
  * Binary32 sums over j in ascending order.  1 <= k <= 32, T*k and rows <= 2^24,
  * N <= 65535*256.  flags: SQ_LAUNCH_PDL.
  */
@@ -622,9 +623,12 @@ typedef struct {
  *            Not used for M <= 64.
  *   base     rows of N f32, ld_base floats apart; NULL: 0.  May be y itself (with
  *            the same row stride); then the rows without an adapter are not
- *            touched.  Otherwise base and y may not overlap.
+ *            touched.  Otherwise rows of base and y may not overlap
+ *            (SQ_ERR_INVALID_ARG; column slices side by side do not).
  *   y        rows of N f32, ld_y floats apart (a slice of a wider projection);
- *            columns outside the slice are left as they were
+ *            columns outside the slice are left as they were.  May not overlap x
+ *            (SQ_ERR_INVALID_ARG), but may be x itself where its rows are as far
+ *            apart (ld_y = K, or M = 1).
  *   workspace  sq_lora_workspace_bytes(bank, M) bytes (0 for M <= 64), 16-byte
  *            aligned; scratch, no zeroing.  Calls that may overlap in time need
  *            their own.

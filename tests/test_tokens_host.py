@@ -253,3 +253,76 @@ def test_an_adapter_workspace_serves_every_shorter_call(L):
             need = L.sq_lora_workspace_bytes(ctypes.byref(b), M)
             assert need >= longest, (S, R, M)
             longest = need
+
+
+def _no_device(rc):
+    """Past every check of arguments: no usable device here, or (on one) not launched."""
+    return rc not in (0, 1, 2, 3, 8)
+
+
+def _at(words):
+    return ctypes.c_void_p((1 << 41) + 4 * words)
+
+
+@pytest.fixture
+def no_gpu():
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("these calls would be launched on made-up addresses")
+
+
+def test_combine_refuses_a_result_over_its_inputs(L, no_gpu):
+    far = _at(1 << 30)
+
+    def call(z=_at(0), rows=8, T=4, N=64, base=None, out=far):
+        return L.sq_combine(z, rows, P, P, T, 2, N, base, out, None, 0, None)
+    assert _no_device(call()) and _no_device(call(base=far))
+    # z holds words [0, 512), out 256 words
+    assert call(out=_at(0)) == 1 and call(out=_at(508)) == 1 and _no_device(call(out=_at(512)))
+    assert call(z=_at(252), out=_at(0)) == 1 and _no_device(call(z=_at(256), out=_at(0)))
+    # base: out itself or apart
+    at = 1 << 30
+    assert call(base=_at(at + 252)) == 1 and call(base=_at(at - 252)) == 1
+    assert _no_device(call(base=_at(at + 256))) and _no_device(call(base=_at(at - 256)))
+
+
+def test_lora_refuses_a_result_over_its_inputs(L, no_gpu):
+    b = sq.SqLoraBank(S=4, R=16, K=256, N=100, type=sq.SQ_TYPE_BF16, A=1 << 45, B=1 << 45, scale=1 << 45, rank=None)
+
+    def call(x=_at(1 << 32), M=32, base=None, ldb=512, y=_at(1 << 30), ldy=512):
+        return L.sq_lora_add(ctypes.byref(b), x, M, P, None, None, base, ldb, y, ldy, None, 0, None, 0, None)
+    o = 1 << 30
+    assert _no_device(call()) and _no_device(call(base=_at(o)))
+    # column slices of one matrix of 512: side by side or over one another, from any row on
+    for col, bad in ((99, 1), (100, 0), (412, 0), (413, 1), (-99, 1), (-100, 0), (512, 1), (-512, 1), (512 * 31 + 50, 1),
+                     (512 * 31 + 100, 0), (512 * 32, 0), (-512 * 31 - 99, 1), (-512 * 32, 0), (512 * 7 + 300, 0)):
+        rc = call(base=_at(o + col))
+        assert (rc == 1) if bad else _no_device(rc), col
+    # other strides: found wherever two rows meet
+    assert call(base=_at(o + 100), ldb=511) == 1 and _no_device(call(base=_at(o + 200), ldb=513, M=3))
+    assert call(base=_at(o + 200), ldb=800, M=3) == 1  # 1000 .. 1099 and 1024 .. 1123
+    assert _no_device(call(base=_at(o + 100), y=_at(o), M=1, ldb=100, ldy=100)) and call(base=_at(o + 99), M=1, ldb=100) == 1
+    # x: rows of 256
+    assert call(x=_at(o)) == 1 and call(x=_at(o + 32 * 512 - 512 + 96)) == 1 and call(x=_at(o - 32 * 256 + 4)) == 1
+    assert _no_device(call(x=_at(o - 32 * 256))) and _no_device(call(x=_at(o + 31 * 512 + 100)))
+    assert _no_device(call(x=_at(o), ldy=256)) and call(x=_at(o + 4), ldy=256) == 1
+
+
+def test_rows_that_overlap_are_found_as_by_listing_them(L, no_gpu):
+    """Small strides against a set of every word."""
+    import itertools
+    import random
+    rng = random.Random(1)
+    for _ in range(400):
+        N, M = rng.randint(1, 6), rng.randint(1, 6)
+        lda, ldb, off = rng.randint(N, 12), rng.randint(N, 12), rng.randint(-40, 40)
+        b = sq.SqLoraBank(S=1, R=1, K=1, N=N, type=sq.SQ_TYPE_F32, A=1 << 45, B=1 << 45, scale=1 << 45, rank=None)
+        o = 1 << 30
+        if off == 0 and lda != ldb:
+            continue  # (refused for its strides)
+        rows = [{o + i * lda + c for i, c in itertools.product(range(M), range(N))},
+                {o + off + i * ldb + c for i, c in itertools.product(range(M), range(N))}]
+        rc = L.sq_lora_add(ctypes.byref(b), _at(1 << 33), M, P, None, None, _at(o + off), ldb, _at(o), lda, None, 0, None,
+                           0, None)
+        bad = off != 0 and bool(rows[0] & rows[1])
+        assert (rc == 1) if bad else _no_device(rc), (N, M, lda, ldb, off)
