@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxDepth = 3;
+constexpr int kMaxDepth = 2;  // (16 rings of three slots and the partial sums do not fit)
 constexpr int kPair = 2;   // tiles per ring slot: neighbours in memory, copied together
 
 struct Params {
@@ -70,23 +70,6 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
       "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Byte k = 0xFF if bit 8k+7 of x is set, else 0.
-__device__ __forceinline__ uint32_t sign_bytes(uint32_t x) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, 0, 0xBA98;" : "=r"(d) : "r"(x));
-  return d;
-}
-// Channels 4w .. 4w+3 of a lane's 32 as +1 / -1 bytes, 0 outside the mask.
-template <bool MASK>
-__device__ __forceinline__ uint32_t trunk_word(uint32_t sign, uint32_t mask, int w) {
-  const uint32_t t = ~sign_bytes(sign << (7 - w)) | 0x01010101u;
-  return MASK ? t & sign_bytes(mask << (7 - w)) : t;
-}
-// The bits of words w and w ^ 4 exchanged (bit 8c + w is channel 4w + c).
-__device__ __forceinline__ uint32_t swap_halves(uint32_t b) {
-  return ((b >> 4) & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
 }
 
 // The tokens of one group: lane l holds those of token l % (8 NT).

@@ -54,6 +54,23 @@ __device__ __forceinline__ bool elect_one() {
   return pred != 0;
 }
 
+// Byte k = 0xFF if bit 8k+7 of x is set, else 0.
+__device__ __forceinline__ uint32_t sign_bytes(uint32_t x) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, 0, 0xBA98;" : "=r"(d) : "r"(x));
+  return d;
+}
+// Channels 4w .. 4w+3 of a lane's 32 as +1 / -1 bytes, 0 outside the mask.
+template <bool MASK>
+__device__ __forceinline__ uint32_t trunk_word(uint32_t sign, uint32_t mask, int w) {
+  const uint32_t t = ~sign_bytes(sign << (7 - w)) | 0x01010101u;
+  return MASK ? t & sign_bytes(mask << (7 - w)) : t;
+}
+// The bits of words w and w ^ 4 exchanged (bit 8c + w is channel 4w + c).
+__device__ __forceinline__ uint32_t swap_halves(uint32_t b) {
+  return ((b >> 4) & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
+}
+
 // Bounds of segment e of a sort of n entries, clamped to them (offsets that do
 // not ascend in [0, n] are reported; no access leaves the arrays).
 __device__ __forceinline__ int2 segment_bounds(const int32_t* offsets, int n, int e, int32_t* status) {

@@ -157,19 +157,6 @@ __device__ __forceinline__ bool aborted(const Aux* aux) {
   return *reinterpret_cast<const volatile int*>(&aux->abort) != 0;
 }
 
-__device__ __forceinline__ uint32_t sign_bytes(uint32_t x) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, 0, 0xBA98;" : "=r"(d) : "r"(x));
-  return d;
-}
-template <bool MASK>
-__device__ __forceinline__ uint32_t trunk_word(uint32_t sign, uint32_t mask, int w) {
-  const uint32_t t = ~sign_bytes(sign << (7 - w)) | 0x01010101u;
-  return MASK ? t & sign_bytes(mask << (7 - w)) : t;
-}
-__device__ __forceinline__ uint32_t swap_halves(uint32_t b) {
-  return ((b >> 4) & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
-}
 // 16 consecutive TMEM columns of this thread's lane: the load, and the wait after
 // which r may be used.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, int (&r)[16]) {
@@ -231,7 +218,7 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
-// One tile: an expert's 128 rows x up to 256 of its places.
+// One tile: an expert's 128 rows x up to kTokens of its places.
 struct Tile {
   int rb0;       // first row block in the stack
   int blocks;    // row blocks of the expert in this tile (1..8)

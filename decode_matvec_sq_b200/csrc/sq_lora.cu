@@ -127,32 +127,28 @@ __device__ __forceinline__ uint32_t upper_pair(float a, float b) {
 }
 __device__ __forceinline__ float below_upper(float v) { return v - __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
 
-// Eight values as T bfloat16 parts (by truncation; T = 3 is exact for binary32,
-// T = 2 for binary16), four pairs each.
-template <int T>
-__device__ __forceinline__ void cut8(float (&v)[8], uint32_t (&o)[T][4]) {
+// Eight values as three bfloat16 parts (by truncation; exact), four pairs each.
+__device__ __forceinline__ void cut8(float (&v)[8], uint32_t (&o)[3][4]) {
 #pragma unroll
-  for (int s = 0; s < T; ++s) {
+  for (int s = 0; s < 3; ++s) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[s][i] = upper_pair(v[2 * i], v[2 * i + 1]);
-    if (s + 1 < T) {
+    if (s < 2) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = below_upper(v[i]);
     }
   }
 }
 
+// Which products a weight type takes: bfloat16 ones as it is, tf32 ones with a binary16
+// weight as one part, or with a binary32 weight cut in two.
 template <class W>
-struct Parts;  // bfloat16 parts of a weight
-template <>
-struct Parts<__nv_bfloat16> { static constexpr int n = 1; };
-template <>
-struct Parts<__half> { static constexpr int n = 2; };
-template <>
-struct Parts<float> { static constexpr int n = 3; };
+constexpr bool kBf16 = std::is_same<W, __nv_bfloat16>::value;
+template <class W>
+constexpr bool kCutWeight = std::is_same<W, float>::value;
 
-// Eight neighbouring elements as they lie in memory, and their bfloat16 parts under
-// a mask (all ones or zero: what is masked may hold anything, NaN included).  The
+// Eight neighbouring elements as they lie in memory, under a mask (all ones or
+// zero: what is masked may hold anything, NaN included).  The
 // loads of a step are issued together, without branches; a row without vector
 // alignment is gathered element by element instead.
 template <class T>
@@ -205,16 +201,6 @@ struct Raw8 {
       }
     }
   }
-  __device__ __forceinline__ void parts(uint32_t (&o)[Parts<T>::n][4]) const {
-    if constexpr (Parts<T>::n == 1) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[0][i] = w[i];
-    } else {
-      float v[8];
-      floats(v);
-      cut8<Parts<T>::n>(v, o);
-    }
-  }
 };
 // Elements i0 .. i0 + 7 of row `row` of a matrix of rows `ld` apart, `len` long; zero
 // unless `live`.  base points at a readable row in any case.  In two halves, so that
@@ -249,7 +235,7 @@ struct Columns;
 template <>
 struct Columns<__nv_bfloat16> {
   uint32_t p[3][4];
-  __device__ __forceinline__ void set(float (&v)[8]) { cut8<3>(v, p); }
+  __device__ __forceinline__ void set(float (&v)[8]) { cut8(v, p); }
   __device__ __forceinline__ void mma(float (&acc)[4], const Raw8<__nv_bfloat16>& w0,
                                       const Raw8<__nv_bfloat16>& w1) const {
     float t[4] = {}, low[4] = {};
@@ -279,7 +265,7 @@ struct Columns32 {  // tf32 parts
     for (int q = 0; q < 4; ++q) {
       uint32_t a[4] = {__float_as_uint(f0[2 * q]), __float_as_uint(f1[2 * q]), __float_as_uint(f0[2 * q + 1]),
                        __float_as_uint(f1[2 * q + 1])};
-      if constexpr (Parts<W>::n == 3) {
+      if constexpr (kCutWeight<W>) {
         uint32_t b[4];
         cut_tf32(f0[2 * q], a[0], b[0]);
         cut_tf32(f1[2 * q], a[1], b[1]);
@@ -646,7 +632,7 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) 
         for (int h = 0; h < 2; ++h) issue_masked<VEC>(xr8[h], xr[h], k, p.K, true);
       };
       auto issue_w = [&](int j, int k) { issue_masked<VEC>(wr8[j], Aa + wrow[j], k, p.K, r0 + 8 * j + gid < rank); };
-      constexpr bool AHEAD = sizeof(W) == 2;  // (no registers for it with binary32 weights)
+      constexpr bool AHEAD = !kCutWeight<W>;  // (no registers for it with binary32 weights)
       issue_x(32 * s0 + 8 * tid4);
       if constexpr (AHEAD) {
 #pragma unroll
@@ -663,10 +649,14 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) 
 #pragma unroll
           for (int h = 0; h < 2; ++h) finish_masked<VEC>(xr8[h], k, p.K, true);
         }
-        if constexpr (Parts<W>::n == 1) {
+        if constexpr (kBf16<W>) {
           uint32_t xa[2][3][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) xr8[h].parts(xa[h]);
+          for (int h = 0; h < 2; ++h) {
+            float v[8];
+            xr8[h].floats(v);
+            cut8(v, xa[h]);
+          }
           issue_x(next);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
@@ -702,7 +692,7 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const Params p) 
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint32_t h0 = __float_as_uint(wv[2 * q]), h1 = __float_as_uint(wv[2 * q + 1]);
-              if constexpr (Parts<W>::n == 3) {
+              if constexpr (kCutWeight<W>) {
                 uint32_t l0, l1;
                 cut_tf32(wv[2 * q], h0, l0);
                 cut_tf32(wv[2 * q + 1], h1, l1);
@@ -755,7 +745,7 @@ constexpr int kRing = 4;        // units of the weight ring
 // bfloat16 parts for bfloat16 weights, two binary16 parts for binary16 ones; for
 // binary32 weights v itself, cut into tf32 parts when it is read.
 template <class W>
-constexpr int kVWords = std::is_same<W, __nv_bfloat16>::value ? 6 : 4;
+constexpr int kVWords = kBf16<W> ? 6 : 4;
 
 // Expand: CTA = one tile of 64 tokens (16 per warp) and a span of columns.  The
 // warp's v lies in shared memory in operand order ([k32 step][part][two 16-byte
@@ -766,7 +756,7 @@ constexpr int kVWords = std::is_same<W, __nv_bfloat16>::value ? 6 : 4;
 template <class W, bool VEC, bool VECY>
 __global__ void __launch_bounds__(kExpandThreads, 4) k_lora_expand(const Params p) {
   constexpr int NV = kVWords<W>;
-  constexpr bool BF = std::is_same<W, __nv_bfloat16>::value, HALF = std::is_same<W, __half>::value;
+  constexpr bool BF = kBf16<W>, HALF = std::is_same<W, __half>::value;
   // [4 warps][Rp / 32][NV][32] of v, [4 warps][8][32] of base, the weight ring, the tile sums
   extern __shared__ __align__(16) uint4 vsm[];
   constexpr int kUnitWords = kBlockCols * 32 * (int)sizeof(W) / 16;  // 16-byte words of a ring unit
@@ -856,7 +846,7 @@ __global__ void __launch_bounds__(kExpandThreads, 4) k_lora_expand(const Params 
             o[h][1][i] = *reinterpret_cast<const uint32_t*>(&lo);
           }
         } else {
-          cut8<3>(v[h], o[h]);
+          cut8(v[h], o[h]);
         }
       }
 #pragma unroll
