@@ -93,11 +93,15 @@ __device__ __forceinline__ int expand_nibble(uint32_t bits) {
   return (int)(((bits & 0xFu) * 0x00204081u) & 0x01010101u);
 }
 
-// v = hi + lo for tf32 products: hi rounded to tf32's 11 bits (a value that would round
-// to infinity, from 2^128 - 2^116 on, to the largest finite one), lo the exact rest, of
-// which the tensor cores read 11 bits.
+// v = hi + lo for tf32 products: hi rounded to tf32's 11 bits, half a step away from
+// zero, lo the exact rest, of which the tensor cores read 11 bits.  A value that would round
+// to infinity (from 2^128 - 2^116 on) takes the largest finite hi: the bits grow with
+// the magnitude, so a minimum for either sign does it.  (The adapters' shrink kernel on
+// binary32 weights takes 19.4 us so, 20.4 with a saturating cvt, 19.9 with a clamp before it.)
+// An infinity then has an infinite lo, a NaN a NaN.
 __device__ __forceinline__ void cut_tf32(float v, uint32_t& hi, uint32_t& lo) {
-  asm("cvt.rna.satfinite.tf32.f32 %0, %1;" : "=r"(hi) : "f"(v));
+  const uint32_t up = (uint32_t)__viaddmin_s32(__float_as_int(v), 0x1000, 0x7F7FFFFF);  // positive
+  hi = min(up, 0xFF7FFFFFu) & 0xFFFFE000u;                                              // negative
   lo = __float_as_uint(v - __uint_as_float(hi));
 }
 __device__ __forceinline__ void cut_tf32(float v, float& hi, float& lo) {
