@@ -498,7 +498,10 @@ cudaError_t launch_kind(const GroupedArgs& a, int sm_count, cudaStream_t stream)
 
 // Measured crossover, few-token kernel against the other, us at 16, 24 and 32 places per
 // expert: 8 experts 4096 x 4096 54 : 63, 63 : 64, 92 : 64; 32 experts 2048 -> 1408 46 : 59,
-// 64 : 60, 79 : 61; 4 experts 4096 -> 14336 93 : 117, 125 : 118, 138 : 118.
+// 64 : 60, 79 : 61; 4 experts 4096 -> 14336 93 : 117, 125 : 118, 138 : 118.  The host knows the
+// average alone; with 60 % of the places at one expert the two meet there too (cold, at 20, 24
+// and 32: 8 experts 4096 x 4096 65 : 70, 74 : 72, 92 : 74; 4 experts 4096 -> 14336 100 : 118,
+// 109 : 117, 141 : 119).
 bool grouped_many(int E, int64_t n) { return n >= 24 * (int64_t)E; }
 
 size_t grouped_workspace_bytes(int E, int K, int64_t n, bool asym, int sm_count) {
@@ -510,7 +513,9 @@ cudaError_t launch_grouped(const GroupedArgs& a, void* workspace, int sm_count, 
     return launch_grouped_tc5(a, workspace, sm_count, stream);
   // Groups of 8 tokens up to 4 places per expert, of 16 above: the second eight
   // cost every tile 60 instructions, a second pass over the weights is rare at four
-  // (16 tokens top-2 of 8 experts 14336 -> 4096: 115 against 139 us).
+  // (16 tokens top-2 of 8 experts 14336 -> 4096: 115 against 139 us).  Groups of 8 : 16, cold, us
+  // at 2, 4, 6, 8 and 12 random places per expert: 8 experts 4096 x 4096 47 : 49, 47 : 49, 55 : 55,
+  // 59 : 53, 84 : 59; 4 experts 4096 -> 14336 59 : 59, 70 : 70, 94 : 88, 98 : 84, 148 : 82.
   if (a.n <= std::max(8, 4 * a.E)) return launch_kind<1>(a, sm_count, stream);
   return launch_kind<2>(a, sm_count, stream);
 }

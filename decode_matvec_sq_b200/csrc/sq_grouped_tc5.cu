@@ -24,15 +24,19 @@
 // are cut into two tf32 parts each, and one stage holds [hi | hi] and [lo] of the
 // weights (written by warps 4-11) and [hi | lo] of the activations (cut by the
 // prologue kernel, brought by TMA); six kind::tf32 MMAs give all products but
-// lo x lo, below 2^-21 of the product.  20 outlier channels cost 8 % of the time (4096
+// lo x lo: with the bits of lo that are not read, at most 2^-21 of a product is left out
+// (the few-token kernel forms these products in binary32).  20 outlier channels cost 8 % of the time (4096
 // places over 8 experts, 4096 -> 14336: 697 us without, 753 us with); on the CUDA
 // cores of the promotion, a row of weights per lane, they cost 30 %.
-// What bounds it: shared memory.  Raw tile in and out, both operands in and out,
-// activations in once and out twice are 160 KB a group, 1250 clocks; a group takes
-// 1300 clocks at 32 tokens (the hand-overs between five roles) and 1800 at 160.
+// What bounds it: the hand-overs between five roles that have two operand stages and two R
+// buffers.  A group takes 1300 clocks at 32 tokens and 1800 at 160.  Raw tile in and out, both
+// operands in and out, activations in once and out twice are 160 KB a group through shared
+// memory, 1250 clocks; but no unit is full: under ncu (8 experts, 4096 places) the tensor
+// pipe is busy 31 % of the time, L1 and shared memory 48 %, DRAM 13 %.
 // Hence the wide tile, one barrier per stage for both operands, and group scales
-// that the promotion reads from memory itself.  At 753 us the whole call is 639
-// TFLOP/s of the layer's products, 0.39 of the measured bf16 rate.
+// that the promotion reads from memory itself.  At 758 us (the same weights again; 790 to 835
+// with other weights at each call) that is 634 TFLOP/s of the layer's products, 0.16 of the
+// int8 rate that the library's probe measures (4086 T op/s), 0.31 for the two products formed.
 // The sums are integers because the tensor cores' binary32 sums are not exact
 // enough: 16-bit operands accumulated over K = 4096 measured 4.4e-6 relative
 // error (a truncation that grows with K; 1.6e-5 at 14336), the integer sums none.

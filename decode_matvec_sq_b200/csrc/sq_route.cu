@@ -20,6 +20,8 @@
 // (10 MB in and out would be 1 us): two launches, in each a chain of load, sort
 // and store.  Experts spread over the lanes (lane + 32 i) took a second reduction
 // per choice, and the chunks' counts read after the chunk's own sort, 23.5 us.
+// Above 524288 entries the reads of the chunks' counts dominate, with the square of the chunks:
+// 524288 ids of 1024 take 49 us, 2097152 453 us, 16777216 21 ms.
 // Combine: one pass, bound by memory (4099 tokens, k = 4, 4096 columns: 6.3 TB/s).
 #include <stdint.h>
 
