@@ -833,8 +833,11 @@ sq_status sq_lora_add(const sq_lora_bank* bank, const float* x, int32_t M, const
     return SQ_ERR_ALIGN;
   const size_t need = lora_workspace_bytes(M, bank->S, bank->R);
   if (need && (!workspace || ws_bytes < need)) return SQ_ERR_WORKSPACE;
+  // (a token's x is read before its y is written, but other tokens' may be read later)
+  const intptr_t at = reinterpret_cast<intptr_t>(y) - reinterpret_cast<intptr_t>(x);
+  const bool in_x = M == 1 || (ld_y == bank->K && at >= 0 && at / 4 + bank->N <= bank->K);
   if ((base && base != y && rows_overlap(base, ld_base, bank->N, y, ld_y, bank->N, M)) ||
-      (!(x == y && (ld_y == bank->K || M == 1)) && rows_overlap(x, bank->K, bank->K, y, ld_y, bank->N, M)))
+      (!in_x && rows_overlap(x, bank->K, bank->K, y, ld_y, bank->N, M)))
     return SQ_ERR_INVALID_ARG;
   DeviceInfo d;
   if ((st = check_device(&d)) != SQ_OK) return st;

@@ -635,9 +635,9 @@ typedef struct {
  *            touched.  Otherwise rows of base and y may not overlap
  *            (SQ_ERR_INVALID_ARG; column slices side by side do not).
  *   y        rows of N f32, ld_y floats apart (a slice of a wider projection);
- *            columns outside the slice are left as they were.  May not overlap x
- *            (SQ_ERR_INVALID_ARG), but may be x itself where its rows are as far
- *            apart (ld_y = K, or M = 1).
+ *            columns outside the slice are left as they were.  May lie in x row by
+ *            row (ld_y = K, row t of y within row t of x), else not overlap it
+ *            (SQ_ERR_INVALID_ARG).
  *   workspace  sq_lora_workspace_bytes(bank, M) bytes (0 for M <= 64), 16-byte
  *            aligned; scratch, no zeroing.  Calls that may overlap in time need
  *            their own.

@@ -305,7 +305,10 @@ def test_lora_refuses_a_result_over_its_inputs(L, no_gpu):
     # x: rows of 256
     assert call(x=_at(o)) == 1 and call(x=_at(o + 32 * 512 - 512 + 96)) == 1 and call(x=_at(o - 32 * 256 + 4)) == 1
     assert _no_device(call(x=_at(o - 32 * 256))) and _no_device(call(x=_at(o + 31 * 512 + 100)))
+    # ... each row of y within the same row of x
     assert _no_device(call(x=_at(o), ldy=256)) and call(x=_at(o + 4), ldy=256) == 1
+    assert _no_device(call(x=_at(o - 156), ldy=256)) and call(x=_at(o - 160), ldy=256) == 1
+    assert _no_device(call(x=_at(o + 4), M=1)) and call(x=_at(o - 156), ldy=512) == 1
 
 
 def test_rows_that_overlap_are_found_as_by_listing_them(L, no_gpu):
